@@ -208,6 +208,99 @@ qift_status qift_decode_linear(const void* x, int64_t tokens, int64_t n_in, int3
                                const float* w_scale, qift_levelset set, int64_t n_out, void* y, qift_dtype out_dt,
                                int8_t* q_out, float* act_scale_out, void* stream);
 
+/*
+ * The paged KV4 cache.  Keys and values of many sequences share one pool of pages:
+ *   codes  : u8 [n_pages][kv_heads][page_size][head_dim/2], for keys and for values; a row holds one
+ *            token of one kv head, packed as by qift_quantize_kv (the lower index in the low nibble).
+ *   scales : fp32 [n_pages][kv_heads][page_size], s = m / 7 of each row.
+ *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096].  Other head dimensions and page
+ *   sizes return QIFT_ERR_UNSUPPORTED.  Slot s is token s % page_size of page s / page_size.
+ *
+ * qift_append_kv -- one layer's new tokens: position rotation of queries and keys, Hadamard rotation
+ * of queries, keys and values, and symmetric per-row INT4 of keys and values into their slots.
+ *   q, k, v   : fp16, token t's heads at q + t * q_stride (elements; a multiple of 8, at least
+ *               heads * head_dim), each head head_dim contiguous values.  q may be NULL (then
+ *               q_heads is 0 and q_out NULL).
+ *   rope      : fp32 [rope_len][rope_dim], 16-byte aligned: for each position rope_dim/2 cosines,
+ *               then rope_dim/2 sines; or NULL: no position rotation (rope_dim is then ignored).
+ *               rope_dim: a multiple of 16, at most head_dim; the values behind it are not rotated.
+ *   rope_interleaved: 0 = value i is paired with value i + rope_dim/2, 1 = value 2i with 2i + 1.
+ *               A pair (a, b) becomes (a c - b s, b c + a s), each operation rounded to fp32.
+ *   positions : int64 [tokens], rows of `rope` (NULL if rope is NULL).
+ *   slots     : int64 [tokens], all different.  A token whose slot is outside the cache (-1 marks
+ *               padding) is not written; one whose position is outside [0, rope_len) is neither
+ *               written nor is its q_out row.  If a slot is named twice, which row it holds is
+ *               unspecified.
+ *   block     : Hadamard block as in qift_rotate, at most head_dim; 0 = none.
+ *   q_out     : fp16 [tokens][q_heads][head_dim] out, the rotated queries that
+ *               qift_paged_attention takes; must not overlap q, k or v.
+ * Arithmetic: rope in fp32, then exactly qift_quantize_kv's of a row of head_dim values (stages of
+ * qift_rotate in fp32, one rounding to fp16, m, 7 / m, codes); with rope NULL the codes and scales
+ * are bit-identical to it.
+ *
+ * qift_gather_kv -- the rows of `slots` read back: (float)code * s in binary32, rotated back by
+ * `block` (0: left in the cache's domain) with qift_rotate's stages, rounded once to fp16.
+ *   k_out, v_out: fp16 [tokens][kv_heads][head_dim].  Rows of slots outside the cache are zeros.
+ */
+qift_status qift_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                           const float* rope, int64_t rope_len, int32_t rope_dim, int32_t rope_interleaved,
+                           const int64_t* positions, const int64_t* slots, int32_t block, void* q_out,
+                           uint8_t* k_cache, float* k_scales, uint8_t* v_cache, float* v_scales, int64_t n_pages,
+                           int32_t page_size, void* stream);
+qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const uint8_t* v_cache,
+                           const float* v_scales, int64_t n_pages, int32_t page_size, int32_t kv_heads,
+                           int32_t head_dim, const int64_t* slots, int64_t tokens, int32_t block, void* k_out,
+                           void* v_out, void* stream);
+
+/*
+ * qift_paged_attention -- causal attention of a ragged batch over the paged KV4 cache, one token a
+ * sequence (decode), several, or whole prompts; optionally with a sliding window and first tokens
+ * that stay visible, and with a prefix that the batch shares.
+ *   q         : fp16, the rotated queries (q_out of qift_append_kv, or queries rotated with
+ *               qift_rotate by the cache's block); strides as there.  q_heads % kv_heads == 0; query
+ *               head i reads kv head i / (q_heads / kv_heads).
+ *   cu_q      : int32 [batch + 1], non-decreasing: sequence b's tokens are rows cu_q[b] ..
+ *               cu_q[b + 1] - 1 of q, at most max_q of them.  NULL: every sequence has exactly max_q
+ *               tokens (tokens == batch * max_q).  Rows of out that belong to no sequence are left
+ *               as they were.
+ *   kv_lens   : int32 [batch], keys of each sequence, the new tokens (appended before) and the
+ *               prefix included: its i-th of n tokens stands at position kv_lens[b] - n + i.
+ *   page_table: int32 [batch][max_pages]: sequence b's pages for positions prefix_len,
+ *               prefix_len + 1, ...  Keys of a page number outside [0, n_pages), and keys beyond the
+ *               table, are not there.
+ *   prefix_table, prefix_len: pages of positions 0 .. prefix_len - 1 (any length), common to all
+ *               sequences and read once for all of them; NULL and 0: no prefix.
+ *   max_kv    : a bound on kv_lens that the host knows, or 0 (then prefix_len + max_pages *
+ *               page_size): it chooses how the work is split, not the result's definition.
+ *   window    : key j is visible from position p if j <= p and j > p - window, or j <= p and
+ *               j < sinks; window 0: if j <= p.
+ *   scale     : softmax scale, usually 1 / sqrt(head_dim).
+ *   block     : the result is rotated back by Hadamard blocks of `block`; 0 leaves it in the cache's
+ *               domain, as qift_quantize_acts with block 0 takes it.
+ *   out       : [tokens][q_heads][head_dim], out_dt QIFT_F16 (one rounding) or QIFT_F32.
+ *   lse       : fp32 [tokens][q_heads] or NULL: log of the sum of exp(scale * q.k) over visible keys.
+ *               A row that sees no key has out 0 and lse -infinity.
+ *   workspace : device memory of at least qift_paged_attention_workspace() bytes (16-byte aligned),
+ *               NULL where that is 0.  Two calls that may run at once, or captured graphs that may,
+ *               need one each.
+ * Scores, the softmax's sums and the weighted sum are fp32; the weights, times their value's scale,
+ * are rounded once to binary16 (11 bits, 2^-12 of each) for the tensor cores.
+ * qift_paged_attention_workspace returns the bytes for a call of these sizes, or -1 if qift_paged_attention
+ * would refuse them.  head_dim, page_size: as above.  (max_pages * page_size + prefix_len) <= 2^30.
+ */
+int64_t qift_paged_attention_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages,
+                                       int32_t max_kv, int32_t prefix_len, int32_t window, int32_t sinks);
+qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, const int32_t* cu_q, int32_t batch, int32_t max_q,
+                                 const uint8_t* k_cache, const float* k_scales, const uint8_t* v_cache,
+                                 const float* v_scales, int64_t n_pages, int32_t page_size,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens,
+                                 int32_t max_kv, const int32_t* prefix_table, int32_t prefix_len, int32_t window,
+                                 int32_t sinks, float scale, int32_t block, void* out, qift_dtype out_dt, float* lse,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+
 /* qift_device_error -- synchronise `stream`, then read and clear the device error word.
  * Returns QIFT_OK, QIFT_ERR_TIMEOUT (a bounded on-chip wait gave up; that call's output is
  * invalid) or QIFT_ERR_CUDA (a CUDA error, or -- in the bounds-checked test build only -- a failed

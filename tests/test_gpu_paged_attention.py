@@ -1,0 +1,533 @@
+"""The paged KV4 cache on the GPU: rows appended and read back against the CPU oracle and the stated order of
+operations, bit for bit; attention against the formula in 64 bits.
+
+Tolerance of attention in the cache's domain, for a row with weights w_j = softmax(u)_j and values v_j, d by d, with
+A = sum_j w_j |v_j|:
+  * each weight times its value's scale is rounded to binary16: 2^-12 of it at most, so 2^-12 A (weights under 2^-22
+    of the largest lose more, but at most 2^-33 of the largest each: 2^-33 n A_max, counted below);
+  * a score's error e_u moves the weights by at most 2 e_u relative: the product adds D + D/2 * 72-fold values in
+    groups of 16, each addition off by at most 2^-22 of partial sums that stay under 80 sum|q|, so
+    e_u <= (D/16 + 1) 2^-22 80 sum|q| max_j s_j scale; the 2^u, scalings and sums add under 2^-17 relative;
+  * a binary16 result is off by 2^-11 of the value (2^-25 where it is subnormal).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import w2a4_gemm_b200 as qg
+from w2a4_gemm_b200 import build
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    build.build()
+    qg.lib()
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def empty_cache(pages, heads, size, d):
+    """A pool that nothing was written to: scales NaN, so that a row read by mistake shows."""
+    c = [torch.full((pages, heads, size, d // 2), 0x77, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.full((pages, heads, size), NAN, device="cuda") for _ in range(2)]
+    return [c[0], s[0], c[1], s[1]]
+
+
+def rope_table(n, dim):
+    a = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def rope_np(x, tab, positions, dim, interleaved):
+    """The stated order of operations in numpy float32 (each rounded)."""
+    x = x.astype(np.float32).copy()
+    c, s = tab[positions][:, None, :dim // 2], tab[positions][:, None, dim // 2:]
+    ia = np.arange(0, dim, 2) if interleaved else np.arange(dim // 2)
+    ib = ia + 1 if interleaved else ia + dim // 2
+    a, b = x[..., ia], x[..., ib]
+    x[..., ia] = a * c - b * s
+    x[..., ib] = b * c + a * s
+    return x
+
+
+def hadamard_np(x, block):
+    if not block:
+        return x
+    y, h = x.astype(np.float32), 1
+    shape = y.shape
+    while h < block:
+        y = y.reshape(-1, 2, h)
+        y = np.stack([y[:, 0] + y[:, 1], y[:, 0] - y[:, 1]], axis=1)
+        h *= 2
+    return y.reshape(shape) * np.float32(1.0 / math.sqrt(block))
+
+
+def quantise_np(x16):
+    x = x16.astype(np.float32)
+    m = np.abs(x).max(-1)
+    inv = np.where(m > 0, np.float32(7) / np.where(m > 0, m, 1), 0).astype(np.float32)
+    q = np.clip(np.rint(x * inv[..., None]), -7, 7).astype(np.int8)
+    return q, (m / np.float32(7)).astype(np.float32)
+
+
+def unpack(p):
+    p = p.view(torch.int8)
+    return torch.stack([(p << 4) >> 4, p >> 4], -1).flatten(-2)
+
+
+# --------------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("d,block", [(64, 64), (64, 0), (128, 128), (128, 2), (128, 16), (128, 32), (256, 256), (256, 64)])
+def test_append_without_rope_is_quantize_kv(d, block):
+    T, H, size = 37, 3, 16
+    x = torch.randn(2, T, H, d, device="cuda", generator=gen(d + block)).half()
+    x[0, 3] = 0
+    cache = empty_cache(5, H, size, d)
+    slots = torch.randperm(5 * size, device="cuda", generator=gen(1))[:T].contiguous()
+    assert qg.qift_append_kv(x[0], x[1], slots, block, *cache) is None
+    for i in range(2):
+        packed, s = oracle.quantize_kv(x[i].reshape(T * H, d).cpu().numpy(), block)
+        at = (slots // size, slice(None), slots % size)
+        assert np.array_equal(cache[2 * i][at].reshape(T * H, d // 2).cpu().numpy(), packed)
+        assert np.array_equal(cache[2 * i + 1][at].flatten().cpu().numpy().view(np.uint32), s.view(np.uint32))
+
+
+@pytest.mark.parametrize("d,rope_dim,interleaved,block,hq,hk,size", [
+    (128, 128, False, 128, 4, 2, 16), (128, 128, True, 128, 5, 1, 32), (64, 32, False, 64, 1, 1, 16),
+    (64, 48, True, 32, 3, 3, 64), (256, 256, False, 256, 2, 1, 128), (256, 64, True, 0, 1, 2, 16),
+    (128, 16, False, 64, 8, 8, 4096), (64, 64, False, 64, 7, 1, 16)])
+def test_append_with_rope_bit_for_bit(d, rope_dim, interleaved, block, hq, hk, size):
+    T, far = 29, 5000
+    g = gen(d + rope_dim)
+    qkv = torch.randn(T, hq + 2 * hk + 1, d, device="cuda", generator=g).half()  # heads behind them belong to no one
+    qkv[:, :, 1] *= 30
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:hq + 2 * hk]
+    pages = T // size + 4
+    cache = empty_cache(pages, hk, size, d)
+    slots = torch.randperm(pages * size, device="cuda", generator=g)[:T].contiguous()
+    slots[4], slots[9], slots[20] = -1, pages * size, -(2 ** 40)
+    positions = torch.randint(0, far, (T,), device="cuda", generator=g)
+    positions[0], positions[1], positions[2], positions[3] = 0, far - 1, far, -1
+    tab = rope_table(far, rope_dim)
+    q_out = torch.full((T, hq, d), 5.0, device="cuda").half()
+    got = qg.qift_append_kv(k, v, slots, block, *cache, q=q, positions=positions, rope=tab.cuda(),
+                            interleaved=interleaved, q_out=q_out)
+    assert got is q_out
+    on = np.ones(T, bool)
+    on[2:4] = False
+    pos = np.clip(positions.cpu().numpy(), 0, far - 1)
+    def turned(x, rope):
+        x = x.cpu().numpy().astype(np.float32)
+        return hadamard_np(rope_np(x, tab.numpy(), pos, rope_dim, interleaved) if rope else x, block).astype(np.float16)
+    want = turned(q, True)
+    want[~on] = 5.0
+    assert np.array_equal(q_out.cpu().numpy().view(np.uint16), want.view(np.uint16))
+    on[[4, 9, 20]] = False
+    kept = torch.from_numpy(on).cuda()
+    at = (slots[kept] // size, slice(None), slots[kept] % size)
+    for i, (x, rope) in enumerate(((k, True), (v, False))):
+        codes, s = quantise_np(turned(x, rope)[on])
+        assert np.array_equal(unpack(cache[2 * i][at]).cpu().numpy(), codes)
+        assert np.array_equal(cache[2 * i + 1][at].cpu().numpy().view(np.uint32), s.view(np.uint32))
+        rest = torch.ones(pages, size, dtype=torch.bool, device="cuda")
+        rest[slots[kept] // size, slots[kept] % size] = False
+        assert torch.isnan(cache[2 * i + 1].movedim(1, 2)[rest]).all()  # no other slot was touched
+        assert (cache[2 * i].movedim(1, 2)[rest] == 0x77).all()
+
+
+@pytest.mark.parametrize("d,block", [(64, 64), (128, 128), (128, 0), (256, 32)])
+def test_gather_bit_for_bit(d, block):
+    H, size, pages = 3, 32, 7
+    g = gen(d)
+    cache = [torch.randint(0, 256, (pages, H, size, d // 2), device="cuda", generator=g).to(torch.uint8),
+             torch.rand(pages, H, size, device="cuda", generator=g)] * 2
+    cache[2] = cache[2].flip(0).contiguous()
+    slots = torch.randint(0, pages * size, (41,), device="cuda", generator=g)
+    slots[5], slots[6] = -1, pages * size
+    got = qg.qift_gather_kv(*cache, slots, block)
+    for i in range(2):
+        at = (slots.clamp(0, pages * size - 1) // size, slice(None), slots.clamp(0, pages * size - 1) % size)
+        want = oracle.dequantize_kv(cache[2 * i][at].reshape(-1, d // 2).cpu().numpy(),
+                                    cache[2 * i + 1][at].flatten().cpu().numpy(), block).reshape(41, H, d)
+        want[5:7] = 0
+        assert np.array_equal(got[i].cpu().numpy(), want)
+
+
+def test_append_then_gather_of_no_tokens():
+    cache = empty_cache(1, 2, 16, 64)
+    x = torch.empty(0, 2, 64, device="cuda").half()
+    s = torch.empty(0, dtype=torch.int64, device="cuda")
+    q = qg.qift_append_kv(x, x, s, 64, *cache, q=x, positions=s, rope=rope_table(4, 64).cuda())
+    k, v = qg.qift_gather_kv(*cache, s, 64)
+    assert q.shape == k.shape == v.shape == (0, 2, 64)
+
+
+# ------------------------------------------------------------------------------------------ attention
+def make(q_lens, kv_lens, hq, hk, d, size, prefix=0, seed=0, gain=1.0):
+    """A ragged batch over a pool whose unused rows hold NaN scales.  kv_lens count the prefix."""
+    g = gen(seed)
+    own = [max(n - prefix, 0) for n in kv_lens]
+    n_own, n_pre = [-(-n // size) for n in own], -(-prefix // size)
+    pages = sum(n_own) + n_pre + 2
+    order = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+    table = torch.full((len(own), max(n_own + [1])), -7, dtype=torch.int32, device="cuda")
+    at = n_pre
+    cache = empty_cache(pages, hk, size, d)
+    def fill(page, count):
+        for i in range(2):
+            x = torch.randn(hk, count, d, device="cuda", generator=g) * (gain if i else 1.0)
+            s = x.abs().amax(-1) / 7
+            c = torch.round(x / s[..., None]).to(torch.int8)
+            cache[2 * i][page, :, :count] = ((c[..., 0::2] & 15) | (c[..., 1::2] << 4)).view(torch.uint8)
+            cache[2 * i + 1][page, :, :count] = s
+    for j in range(n_pre):
+        fill(int(order[j]), min(size, prefix - j * size))
+    for b, n in enumerate(own):
+        for j in range(n_own[b]):
+            table[b, j] = order[at]
+            fill(int(order[at]), min(size, n - j * size))
+            at += 1
+    T = sum(q_lens)
+    return dict(q=torch.randn(T, hq, d, device="cuda", generator=g).half(),
+                cu_q=torch.tensor([0] + list(np.cumsum(q_lens)), dtype=torch.int32, device="cuda"),
+                max_q=max(q_lens + [1]), cache=cache, table=table,
+                kv_lens=torch.tensor(kv_lens, dtype=torch.int32, device="cuda"),
+                prefix_table=order[:n_pre].contiguous() if prefix else None, prefix=prefix)
+
+
+def reference(m, window=0, sinks=0, scale=None, prefix=None):
+    """The formula in 64 bits: (out in the cache's domain, lse, A, e_u) per row."""
+    kc, ks, vc, vs = m["cache"]
+    pages, hk, size, half = kc.shape
+    d = 2 * half
+    q = m["q"].double()
+    T, hq, _ = q.shape
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    out, A = torch.zeros(2, T, hq, d, dtype=torch.float64, device="cuda")
+    lse = torch.full((T, hq), -math.inf, dtype=torch.float64, device="cuda")
+    e_u = torch.zeros(T, hq, dtype=torch.float64, device="cuda")
+    cu, lens, P = m["cu_q"].tolist(), m["kv_lens"].tolist(), m["prefix"]
+    for b, n in enumerate(lens):
+        nq = cu[b + 1] - cu[b]
+        if not nq:
+            continue
+        def rows(c, s, h):
+            pre = m["prefix_table"][:-(-P // size)].long() if P else []
+            parts = []
+            if P:
+                parts.append((unpack(c[pre, h]).double() * s[pre, h].double()[..., None]).reshape(-1, d)[:min(P, n)])
+            if n > P:
+                t = m["table"][b, :-(-(n - P) // size)].long()
+                x = torch.zeros(len(t), size, d, dtype=torch.float64, device="cuda")
+                good = (t >= 0) & (t < pages)
+                x[good] = unpack(c[t[good], h]).double() * s[t[good], h].double()[..., None]
+                x[~good] = NAN
+                parts.append(x.reshape(-1, d)[:n - P])
+            return torch.cat(parts) if parts else torch.zeros(0, d, dtype=torch.float64, device="cuda")
+        i = torch.arange(nq, device="cuda")[:, None] + n - nq
+        j = torch.arange(n, device="cuda")[None, :]
+        see = (j <= i) & ((j > i - window) | (j < sinks) if window else torch.ones_like(j <= i))
+        for h in range(hk):
+            k, v = rows(kc, ks, h), rows(vc, vs, h)
+            lost = torch.isnan(k).any(-1)  # pages that are not there
+            vis = see & ~lost[None]
+            k, v = torch.nan_to_num(k), torch.nan_to_num(v)
+            for x in range(h * hq // hk, (h + 1) * hq // hk):
+                u = (q[cu[b]:cu[b + 1], x] @ k.T * scale).masked_fill(~vis, -math.inf)
+                l = torch.logsumexp(u, -1) if n else torch.full((nq,), -math.inf, dtype=torch.float64, device="cuda")
+                w = torch.where(vis, torch.exp(u - torch.where(l.isinf(), 0, l)[:, None]), 0)
+                out[cu[b]:cu[b + 1], x], A[cu[b]:cu[b + 1], x] = w @ v, w @ v.abs()
+                lse[cu[b]:cu[b + 1], x] = l
+                s_max = torch.nan_to_num(k.abs().amax() / 7) if n else 0
+                e_u[cu[b]:cu[b + 1], x] = (d / 16 + 1) * 2.0 ** -22 * 80 * q[cu[b]:cu[b + 1], x].abs().sum(-1) * s_max * scale
+    return out, lse, A, e_u
+
+
+def bound(A, e_u, ref, half):
+    t = A * (2.0 ** -12 + 2 * e_u[..., None] + 2.0 ** -17) + A.amax(-1, keepdim=True) * 2.0 ** -16
+    return t + (2.0 ** -11 * ref.abs() + 2.0 ** -25 if half else 2.0 ** -22 * ref.abs() + 1e-38)
+
+
+def call(m, **kw):
+    return qg.qift_paged_attention(m["q"], m["cu_q"], m["max_q"], *m["cache"], m["table"], m["kv_lens"],
+                                   prefix_table=m["prefix_table"], prefix_len=m["prefix"], **kw)
+
+
+def check(m, window=0, sinks=0, scale=None, dtypes=(torch.float32, torch.float16), **kw):
+    ref, lse, A, e_u = reference(m, window, sinks, scale)
+    cu = m["cu_q"].tolist()
+    for dt in dtypes:
+        out = torch.full(m["q"].shape, 77.0, device="cuda", dtype=dt)
+        l = torch.full(m["q"].shape[:2], 77.0, device="cuda")
+        call(m, window=window, sinks=sinks, scale=scale, out=out, out_dtype=dt, lse=l, **kw)
+        inside = slice(cu[0], cu[-1])
+        err = (out.double() - ref).abs()[inside]
+        tol = bound(A, e_u, ref, dt == torch.float16)[inside]
+        assert not torch.isnan(err).any()
+        assert (err <= tol).all(), (float((err / tol).max()), (err / tol).flatten(1).amax(1).tolist()[:40])
+        assert (out[:cu[0]] == 77).all() and (out[cu[-1]:] == 77).all()
+        none = lse[inside].isinf()
+        assert torch.equal(l[inside].isinf() & (l[inside] < 0), none)
+        assert (out[inside][none] == 0).all()
+        assert ((l.double() - lse)[inside][~none].abs() <= (e_u[inside] + 2.0 ** -16 + lse[inside].abs() * 2.0 ** -20)[~none]).all()
+    return out
+
+
+LAYOUTS = [(4, 1, 128, 16), (8, 8, 128, 32), (7, 1, 64, 64), (16, 1, 64, 16), (6, 3, 256, 16), (24, 1, 128, 128), (16, 1, 256, 32)]
+
+
+@pytest.mark.parametrize("hq,hk,d,size", LAYOUTS)
+def test_decode_ragged(hq, hk, d, size):
+    lens = [1, 0, 2, 15, 16, 17, 31, 32, 33, 64, 127, 128, 129, 500, 700]
+    check(make([1] * len(lens), lens, hq, hk, d, size, seed=d + hq))
+
+
+@pytest.mark.parametrize("hq,hk,d,size", LAYOUTS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (37, 0), (64, 4), (100, 70), (2000, 3)])
+def test_decode_window(hq, hk, d, size, window, sinks):
+    lens = [1, 3, 36, 37, 38, 41, 64, 65, 101, 170, 333, 900]
+    check(make([1] * len(lens), lens, hq, hk, d, size, seed=window), window, sinks, dtypes=(torch.float32,))
+
+
+@pytest.mark.parametrize("hq,hk,d,size", LAYOUTS)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 4)])
+def test_several_tokens_and_rows_that_see_nothing(hq, hk, d, size, window, sinks):
+    # more tokens than keys: the first of them stand before the sequence's start and see nothing
+    m = make([3, 0, 5, 1, 2, 8, 4], [100, 40, 3, 0, 260, 8, 133], hq, hk, d, size, seed=3)
+    check(m, window, sinks)
+
+
+@pytest.mark.parametrize("hq,hk,d,size", LAYOUTS[:5])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+def test_prompts(hq, hk, d, size, window, sinks):
+    check(make([130, 65, 1, 257], [130, 200, 77, 700], hq, hk, d, size, seed=5), window, sinks)
+
+
+@pytest.mark.parametrize("hq,hk,d,size", LAYOUTS)
+@pytest.mark.parametrize("prefix,window,sinks", [(1, 0, 0), (64, 0, 0), (301, 0, 0), (301, 40, 5), (1000, 400, 0), (77, 200, 90)])
+def test_shared_prefix(hq, hk, d, size, prefix, window, sinks):
+    own = [1, 5, 16, 40, 129, 2, 33]
+    m = make([1, 1, 2, 3, 1, 0, 1], [prefix + n for n in own], hq, hk, d, size, prefix=prefix, seed=prefix)
+    check(m, window, sinks, dtypes=(torch.float32,))
+
+
+def test_sequences_that_end_inside_the_prefix():
+    m = make([1, 2, 1, 1, 4], [10, 64, 200, 0, 2], 8, 2, 128, 16, prefix=150, seed=9)
+    check(m)
+    check(m, 20, 3)
+
+
+def test_prefix_for_many_rows_equals_its_keys_in_every_table():
+    # The same keys, once as a prefix and once as pages that all tables begin with: the same sums in another order.
+    hq, hk, d, size, prefix = 32, 8, 128, 16, 640
+    m = make([1] * 40, [prefix + 3 * b for b in range(40)], hq, hk, d, size, prefix=prefix, seed=2)
+    a = check(m, dtypes=(torch.float32,))
+    whole = dict(m, table=torch.cat([m["prefix_table"][None].expand(40, -1), m["table"]], 1).contiguous(),
+                 prefix_table=None, prefix=0)
+    b = check(whole, dtypes=(torch.float32,))
+    assert (a - b).abs().max() < 2e-3 * b.abs().max()
+
+
+def test_long_sequence_is_split():
+    m = make([1, 1], [20011, 5], 8, 2, 128, 64, seed=1)
+    check(m)
+    check(m, max_kv=64)  # a bound that is wrong changes how the work is split, not what it is
+
+
+def test_result_rotated_back():
+    m = make([1, 7, 40], [90, 30, 333], 8, 2, 128, 16, seed=4)
+    x = call(m, out_dtype=torch.float32)
+    for block in (2, 16, 128):
+        y = call(m, out_dtype=torch.float32, block=block)
+        want = torch.from_numpy(hadamard_np(x.cpu().numpy(), block)).double()
+        # the same sums before the rotation; its log2(block) stages and the last product round once each
+        rms = x.double().pow(2).mean(-1, keepdim=True).sqrt().cpu() * math.sqrt(block)
+        assert ((y.double().cpu() - want).abs() <= 2.0 ** -20 * rms + 1e-9).all()
+
+
+@pytest.mark.parametrize("gain", [1e-6, 1e3])
+def test_small_and_large_values(gain):
+    m = make([1, 3], [300, 90], 8, 2, 128, 16, seed=6, gain=gain)
+    ref, _, A, e_u = reference(m)
+    out = call(m, out_dtype=torch.float32)
+    assert ((out.double() - ref).abs() <= bound(A, e_u, ref, False)).all()
+
+
+def test_values_of_very_different_size_and_zero_rows():
+    m = make([1, 2], [200, 64], 4, 1, 128, 16, seed=8)
+    vs = m["cache"][3]
+    vs[:, :, 0::3] = 0.0                                   # tokens whose values are all zero
+    vs[:, :, 1::3] *= 1e-5
+    m["cache"][1][0, :, 3] = 0.0                           # a key that is all zero
+    check(m, dtypes=(torch.float32,))
+    vs.zero_()
+    assert (call(m) == 0).all()
+
+
+def test_peaked_scores():
+    m = make([2, 1], [500, 90], 8, 2, 128, 16, seed=10)
+    m["q"] *= 40
+    check(m)
+
+
+def test_rows_outside_every_sequence_are_left():
+    m = make([1, 2, 1], [40, 50, 60], 4, 2, 64, 16, seed=11)
+    m["q"] = torch.cat([m["q"], m["q"].flip(0)])           # four rows of padding behind
+    check(m)
+    m["cu_q"] += 2                                          # ... and two in front
+    check(m)
+
+
+def test_pages_that_are_not_there():
+    m = make([1, 1, 1], [100, 80, 40], 4, 2, 128, 16, seed=12)
+    m["table"][0, 2], m["table"][1, 0], m["table"][2, 0] = -1, 2 ** 31 - 1, m["cache"][0].shape[0]
+    check(m)
+    short = dict(m, table=m["table"][:, :3].contiguous())   # keys beyond the table are not there either
+    a = call(short, out_dtype=torch.float32)
+    assert torch.isfinite(a).all()
+
+
+def test_contradicting_offsets_stay_inside():
+    m = make([2, 2], [40, 50], 4, 2, 64, 16, seed=13)
+    for cu in ([0, 3, 2], [-5, 2, 4], [0, 2, 400], [4, 4, 4]):
+        out = torch.full((4, 4, 64), 7.0, device="cuda").half()
+        call(dict(m, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda")), out=out)
+    call(dict(m, kv_lens=torch.tensor([-3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")))
+    torch.cuda.synchronize()
+
+
+def test_uniform_batch_without_offsets():
+    m = make([3] * 5, [9, 70, 33, 3, 128], 8, 4, 128, 16, seed=14)
+    a, b = call(m), call(dict(m, cu_q=None))
+    assert torch.equal(a, b)
+
+
+def test_strided_queries():
+    m = make([1, 4], [77, 200], 8, 2, 128, 16, seed=15)
+    wide = torch.randn(5, 13, 128, device="cuda").half()
+    wide[:, 2:10] = m["q"]
+    assert torch.equal(call(m), call(dict(m, q=wide[:, 2:10])))
+
+
+def test_a_pool_past_32_bits():
+    d, hk, size = 128, 8, 64
+    pages = 2 ** 31 // (hk * size * d // 2) + 70            # over 2^31 bytes of codes
+    m = make([1], [150], 8, hk, d, size, seed=16)
+    small = m["cache"]
+    big = [torch.zeros(pages, *t.shape[1:], dtype=t.dtype, device="cuda") for t in small]
+    shift = pages - small[0].shape[0]
+    for b, s in zip(big, small):
+        b[shift:] = s
+    want = call(m)
+    got = call(dict(m, cache=big, table=m["table"] + shift))
+    assert torch.equal(want, got)
+    slots = (torch.arange(3, device="cuda") + pages * size - 3)
+    x = torch.randn(3, hk, d, device="cuda").half()
+    qg.qift_append_kv(x, x, slots, 128, *big)
+    k, v = qg.qift_gather_kv(*big, slots, 128)
+    err = (k.float() - x.float()).abs()
+    assert torch.equal(k, v) and err.max() < 0.5 * x.float().norm(dim=-1).max() / 7
+
+
+def test_other_stream_and_captured_graphs():
+    m = make([1, 1], [9000, 4000], 8, 2, 128, 16, seed=17)
+    want = call(m)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = call(m, stream=s)
+    s.synchronize()
+    assert torch.equal(want, got)
+    m2 = dict(m, q=m["q"].flip(0).contiguous())
+    want2 = call(m2)
+    graphs, outs = [], []
+    for x in (m, m2):                                       # each captures a workspace of its own
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(call(x))
+        graphs.append(gr)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            graphs[0].replay()
+        with torch.cuda.stream(b):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want2)
+    m["kv_lens"][0] = 1234                                  # lengths are read on the device, at replay
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], call(m))
+
+
+def test_same_call_twice_gives_the_same_bits():
+    m = make([1] * 6 + [90], [3000, 40, 777, 5000, 1, 60, 4000], 32, 8, 128, 16, prefix=0, seed=18)
+    assert torch.equal(call(m), call(m))
+
+
+def test_refusals_leave_the_result_alone():
+    m = make([1], [40], 4, 2, 128, 16)
+    out = torch.full((1, 4, 128), 3.0, device="cuda").half()
+    for bad in (dict(q=m["q"].float()), dict(q=m["q"][:, :, :64]), dict(q=m["q"].transpose(0, 1)), dict(kv_lens=m["kv_lens"].long()),
+                dict(table=m["table"][0]), dict(cu_q=m["cu_q"][:1]), dict(prefix=16), dict(max_q=-1)):
+        with pytest.raises((ValueError, qg.QiftError)):
+            call(dict(m, **bad), out=out)
+    with pytest.raises(ValueError):
+        call(m, out=out[:, :2])
+    with pytest.raises(ValueError):
+        call(m, out=out, out_dtype=torch.float32)
+    with pytest.raises(qg.QiftError):
+        call(m, out=out, block=3)
+    torch.cuda.synchronize()
+    assert (out == 3).all()
+
+
+# ----------------------------------------------------------------------------------- as it would be used
+@pytest.mark.parametrize("window,sinks", [(0, 0), (48, 4)])
+def test_a_layer_prompt_then_single_tokens(window, sinks):
+    """Projections by the W2A4 linear, rows appended, attention, and the output projection fed in the rotated
+    domain: a prompt and then tokens one by one give the same rows as the whole text at once."""
+    hq, hk, d, n_in, size = 8, 2, 128, 512, 16
+    T, block = 70, 128
+    g = gen(21)
+    w = torch.randn((hq + 2 * hk) * d, n_in, device="cuda", generator=g) * 0.02
+    wo = torch.randn(n_in, hq * d, device="cuda", generator=g) * 0.02
+    c, s, _ = qg.qift_quantize_weights(qg.qift_rotate(w, block), "qift")
+    co, so, _ = qg.qift_quantize_weights(qg.qift_rotate(wo, block), "qift")
+    rope = rope_table(128, d).cuda()
+    x = torch.randn(T, n_in, device="cuda", generator=g).half()
+    table = torch.randperm(8, device="cuda", generator=g).to(torch.int32)[None, :5].contiguous()
+
+    def layer(cache, x, first):
+        n = x.shape[0]
+        qx, sx = qg.qift_quantize_acts(x, block)
+        qkv = qg.qift_linear(qx, sx, c, s, "qift").view(n, hq + 2 * hk, d)
+        at = torch.arange(first, first + n, device="cuda")
+        slots = table[0].long()[at // size] * size + at % size
+        q = qg.qift_append_kv(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, block, *cache, q=qkv[:, :hq], positions=at,
+                              rope=rope)
+        o = qg.qift_paged_attention(q, None, n, *cache, table, torch.tensor([first + n], device="cuda", dtype=torch.int32),
+                                    window=window, sinks=sinks)
+        qo, sa = qg.qift_quantize_acts(o.view(n, hq * d), 0)
+        return o, qg.qift_linear(qo, sa, co, so, "qift")
+
+    one, two = empty_cache(8, hk, size, d), empty_cache(8, hk, size, d)
+    o_all, y_all = layer(one, x, 0)
+    parts = [layer(two, x[:40], 0)] + [layer(two, x[i:i + 1], i) for i in range(40, T)]
+    for a, b in zip(one, two):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))    # the same rows in the cache
+    o_parts = torch.cat([p[0] for p in parts]).float()
+    # each side is off by at most the bound above; values are at most 7 * max scale
+    assert (o_all.float() - o_parts).abs().max() <= 2 * (2.0 ** -11 + 2.0 ** -12 + 2e-3) * 7 * one[3][~one[3].isnan()].max()
+    assert torch.isfinite(y_all).all() and y_all.shape == (T, n_in)

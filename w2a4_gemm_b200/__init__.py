@@ -13,6 +13,7 @@ these functions raise.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 import torch
@@ -53,6 +54,13 @@ def lib() -> C.CDLL:
         L.qift_dequantize_kv.argtypes = [vp, vp, i64, i64, i32, vp, vp]
         L.qift_linear.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, vp, i32, vp]
         L.qift_decode_linear.argtypes = [vp, i64, i64, i32, vp, vp, i32, i64, vp, i32, vp, vp, vp]
+        L.qift_append_kv.argtypes = [vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, vp, i64, i32, i32, vp, vp, i32, vp,
+                                     vp, vp, vp, vp, i64, i32, vp]
+        L.qift_gather_kv.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, vp, i64, i32, vp, vp, vp]
+        L.qift_paged_attention_workspace.argtypes = [i64] + [i32] * 11
+        L.qift_paged_attention_workspace.restype = i64
+        L.qift_paged_attention.argtypes = [vp, i64, i64, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp, i64, i32, vp, i32,
+                                           vp, i32, vp, i32, i32, i32, C.c_float, i32, vp, i32, vp, vp, i64, vp]
         L.qift_device_error.argtypes = [vp, C.POINTER(i32)]
         L.qift_debug_set_wait_limit.argtypes = [i64]
         L.qift_debug_stall_next_gemm.argtypes = []
@@ -68,6 +76,7 @@ def lib() -> C.CDLL:
                      "qift_quantize_weights_asym", "qift_quantize_acts",
                      "qift_quantize_kv", "qift_dequantize_kv",
                      "qift_linear", "qift_decode_linear",
+                     "qift_append_kv", "qift_gather_kv", "qift_paged_attention",
                      "qift_device_error", "qift_debug_set_wait_limit", "qift_debug_stall_next_gemm",
                      "qift_debug_stall_next_one_token",
                      "qift_debug_set_linear_path", "qift_debug_set_pdl", "qift_debug_check_line"):
@@ -338,6 +347,197 @@ def qift_decode_linear(x: torch.Tensor, block: int, codes: torch.Tensor, w_scale
                                         dt, _ptr(q_out), _ptr(act_scale_out), _stream(stream, dev)),
                "qift_decode_linear")
     return y
+
+
+def _head_rows(t: torch.Tensor, name: str) -> int:
+    """Checks a [tokens, heads, head_dim] fp16 tensor whose heads lie one behind the other (a slice of a
+    projection's output is one); returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.dtype != torch.float16:
+        raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
+    n, h, d = t.shape
+    row, head, one = t.stride()
+    if n <= 1:
+        row = h * d
+    if (one != 1 and d > 1) or (head != d and h > 1) or row < h * d:
+        raise ValueError(f"{name} must hold each token's heads one behind the other, got strides {t.stride()}")
+    return row
+
+
+def _cache(k_cache, k_scales, v_cache, v_scales):
+    """Checks a paged cache; returns (pages, kv_heads, page_size, head_dim)."""
+    _cuda(k_cache, "k_cache", torch.uint8)
+    _cuda(v_cache, "v_cache", torch.uint8)
+    _cuda(k_scales, "k_scales", torch.float32)
+    _cuda(v_scales, "v_scales", torch.float32)
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim / 2], got shape {tuple(k_cache.shape)}")
+    _shape(v_cache, "v_cache", k_cache.shape)
+    _shape(k_scales, "k_scales", k_cache.shape[:3])
+    _shape(v_scales, "v_scales", k_cache.shape[:3])
+    pages, heads, size, half = k_cache.shape
+    return pages, heads, size, 2 * half
+
+
+class _on:
+    """Makes `dev` the current device for a launch; nothing where it is already."""
+
+    def __init__(self, dev):
+        self.other = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *e):
+        if self.other is not None:
+            self.other.__exit__(*e)
+
+
+def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block: int, k_cache: torch.Tensor,
+                   k_scales: torch.Tensor, v_cache: torch.Tensor, v_scales: torch.Tensor,
+                   q: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                   rope: torch.Tensor | None = None, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor | None:
+    """New tokens into a paged KV4 cache: position rotation, Hadamard rotation by ``block``, INT4 rows.
+
+    ``k``, ``v`` (and ``q``) are fp16 ``[tokens, heads, head_dim]``, slices of one projection's output as they
+    are.  ``k_cache``/``v_cache`` uint8 ``[pages, kv_heads, page_size, head_dim / 2]`` and ``k_scales``/``v_scales``
+    fp32 ``[pages, kv_heads, page_size]`` are written at ``slots`` (int64, ``page * page_size + offset``; -1 =
+    padding).  ``rope`` fp32 ``[positions, rope_dim]`` holds cosines, then sines, and ``positions`` (int64) its row
+    for each token.  Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
+    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    ks, vs = _head_rows(k, "k"), _head_rows(v, "v")
+    T = k.shape[0]
+    _shape(k, "k", (T, kv_heads, d))
+    _shape(v, "v", (T, kv_heads, d))
+    _shape(_cuda(slots, "slots", torch.int64), "slots", (T,))
+    qs = hq = 0
+    if q is not None:
+        qs, hq = _head_rows(q, "q"), q.shape[1]
+        _shape(q, "q", (T, hq, d))
+        if q_out is not None:
+            _shape(_cuda(q_out, "q_out", torch.float16), "q_out", (T, hq, d))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope_len = rope_dim = 0
+    if rope is not None:
+        rope_len, rope_dim = _2d(_cuda(rope, "rope", torch.float32), "rope").shape
+        if positions is None:
+            raise ValueError("rope needs positions")
+        _shape(_cuda(positions, "positions", torch.int64), "positions", (T,))
+    dev = _same_device(("k", k), ("v", v), ("slots", slots), ("k_cache", k_cache), ("k_scales", k_scales),
+                       ("v_cache", v_cache), ("v_scales", v_scales), ("q", q), ("q_out", q_out), ("rope", rope),
+                       ("positions", positions if rope is not None else None))
+    if q is not None and hq == 0:
+        raise ValueError("q must have at least one head")
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.float16, device=dev)
+    with _on(dev):
+        _check(lib().qift_append_kv(_ptr(q) if T else None, qs, _ptr(k), ks, _ptr(v), vs, T, hq if T else 0, kv_heads, d,
+                                    _ptr(rope) if T else None, rope_len, rope_dim, 1 if interleaved else 0,
+                                    _ptr(positions) if rope is not None else None, _ptr(slots), block,
+                                    _ptr(q_out) if T else None, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
+                                    _ptr(v_scales), pages, size, _stream(stream, dev)), "qift_append_kv")
+    return q_out
+
+
+def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch.Tensor, v_scales: torch.Tensor,
+                   slots: torch.Tensor, block: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rows of a paged KV4 cache read back, rotated back by ``block`` (0: in the cache's domain): fp16
+    ``(k, v)``, each ``[tokens, kv_heads, head_dim]``; zeros for slots outside the cache."""
+    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    _cuda(slots, "slots", torch.int64)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be 1-D, got shape {tuple(slots.shape)}")
+    T = slots.shape[0]
+    dev = _same_device(("k_cache", k_cache), ("k_scales", k_scales), ("v_cache", v_cache), ("v_scales", v_scales),
+                       ("slots", slots))
+    k, v = torch.empty((2, T, kv_heads, d), dtype=torch.float16, device=dev).unbind(0)
+    with _on(dev):
+        _check(lib().qift_gather_kv(_ptr(k_cache), _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), pages, size, kv_heads,
+                                    d, _ptr(slots), T, block, _ptr(k), _ptr(v), _stream(stream, dev)),
+               "qift_gather_kv")
+    return k, v
+
+
+def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int, k_cache: torch.Tensor,
+                         k_scales: torch.Tensor, v_cache: torch.Tensor, v_scales: torch.Tensor,
+                         page_table: torch.Tensor, kv_lens: torch.Tensor, window: int = 0, sinks: int = 0,
+                         prefix_table: torch.Tensor | None = None, prefix_len: int = 0, max_kv: int = 0,
+                         scale: float | None = None, block: int = 0, out_dtype=torch.float16,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of a ragged batch over a paged KV4 cache.
+
+    ``q`` fp16 ``[tokens, q_heads, head_dim]`` holds rotated queries (what ``qift_append_kv`` returns); sequence
+    ``b`` has rows ``cu_q[b] .. cu_q[b + 1] - 1`` (int32; None: ``max_q`` rows each), at most ``max_q``, and
+    ``kv_lens[b]`` keys (int32, the new tokens and the prefix included) in the pages ``page_table[b]`` (int32
+    ``[batch, max_pages]``).  ``window``: keys a row sees up to its own (0: all), besides the first ``sinks``.
+    ``prefix_table`` (int32): pages of the ``prefix_len`` first keys that all sequences share.  ``block``: the
+    result is rotated back by Hadamard blocks of this size (0: left rotated, as ``qift_quantize_acts`` with block
+    0 takes it).  ``lse`` (fp32 ``[tokens, q_heads]``), if given, receives the log-sum-exp.  ``workspace`` (uint8,
+    ``qift_paged_attention_workspace`` bytes) is allocated on the call's stream if not given.  Rows of a new result
+    that belong to no sequence are not initialised."""
+    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
+    qs = _head_rows(q, "q")
+    T, hq, _ = q.shape
+    _shape(q, "q", (T, hq, d))
+    _2d(_cuda(page_table, "page_table", torch.int32), "page_table")
+    B, max_pages = page_table.shape
+    _shape(_cuda(kv_lens, "kv_lens", torch.int32), "kv_lens", (B,))
+    if cu_q is not None:
+        _shape(_cuda(cu_q, "cu_q", torch.int32), "cu_q", (B + 1,))
+    elif T != B * max_q:
+        raise ValueError(f"without cu_q, q must have batch * max_q = {B * max_q} rows, got {T}")
+    if prefix_table is not None:
+        _at_least(_cuda(prefix_table, "prefix_table", torch.int32), "prefix_table", -(-prefix_len // size))
+    elif prefix_len != 0:
+        raise ValueError("prefix_len needs prefix_table")
+    if out_dtype not in (torch.float16, torch.float32):
+        raise ValueError("out_dtype must be torch.float16 or torch.float32")
+    if out is not None:
+        _shape(_cuda(out, "out", out_dtype), "out", (T, hq, d))
+    if lse is not None:
+        _shape(_cuda(lse, "lse", torch.float32), "lse", (T, hq))
+    dev = _same_device(("q", q), ("cu_q", cu_q), ("k_cache", k_cache), ("k_scales", k_scales), ("v_cache", v_cache),
+                       ("v_scales", v_scales), ("page_table", page_table), ("kv_lens", kv_lens),
+                       ("prefix_table", prefix_table), ("out", out), ("lse", lse), ("workspace", workspace))
+    L = lib()
+    need = L.qift_paged_attention_workspace(T, hq, kv_heads, d, B, max_q, size, max_pages, max_kv, prefix_len, window,
+                                            sinks)
+    if workspace is not None:
+        _at_least(_cuda(workspace, "workspace", torch.uint8), "workspace", max(need, 0))
+    elif need > 0:
+        if stream is None or stream == torch.cuda.current_stream(dev):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:  # freed, and used again, in the order of the stream that runs the kernels
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    y = torch.empty((T, hq, d), dtype=out_dtype, device=dev) if out is None else out
+    with _on(dev):
+        _check(L.qift_paged_attention(_ptr(q), qs, T, hq, kv_heads, d, _ptr(cu_q), B, max_q, _ptr(k_cache),
+                                      _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), pages, size, _ptr(page_table),
+                                      max_pages, _ptr(kv_lens), max_kv, _ptr(prefix_table), prefix_len, window, sinks,
+                                      1.0 / math.sqrt(d) if scale is None else scale, block, _ptr(y),
+                                      QIFT_F16 if out_dtype == torch.float16 else QIFT_F32, _ptr(lse), _ptr(workspace),
+                                      workspace.numel() if workspace is not None else 0, _stream(stream, dev)),
+               "qift_paged_attention")
+    return y
+
+
+def qift_paged_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, batch: int, max_q: int,
+                                   page_size: int, max_pages: int, max_kv: int = 0, prefix_len: int = 0,
+                                   window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace that ``qift_paged_attention`` needs for these sizes; raises if it would refuse them."""
+    n = lib().qift_paged_attention_workspace(tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages,
+                                             max_kv, prefix_len, window, sinks)
+    if n < 0:
+        raise ValueError("qift_paged_attention would refuse these sizes")
+    return n
 
 
 def qift_device_error(stream=None) -> tuple[int, int]:

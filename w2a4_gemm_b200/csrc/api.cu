@@ -23,6 +23,54 @@ qift_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QIFT_OK : QIFT_
 
 bool valid_block(int64_t b) { return is_pow2(b) && b >= 2 && b <= 4096; }
 
+bool head_block(int32_t b, int32_t d) { return b == 0 || (valid_block(b) && d % b == 0); }
+
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+// Layouts of the paged cache: QIFT_OK if the library has kernels for them.
+qift_status cache_shape(int64_t n_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
+    if (n_pages < 0 || page_size <= 0 || kv_heads <= 0 || head_dim <= 0) return QIFT_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QIFT_ERR_UNSUPPORTED;
+    if (!is_pow2(page_size) || page_size < 16 || page_size > 4096) return QIFT_ERR_UNSUPPORTED;
+    if (kv_heads > 1 << 16 || n_pages > INT64_MAX / kv_heads / page_size / head_dim) return QIFT_ERR_UNSUPPORTED;
+    return QIFT_OK;
+}
+int log2_of(int32_t v) {
+    int l = 0;
+    while ((1 << l) < v) ++l;
+    return l;
+}
+
+// Sizes of an attention call; `a` receives them.
+qift_status attention_sizes(qift::AttentionArgs* a, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                            int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages, int32_t max_kv,
+                            int32_t prefix_len, int32_t window, int32_t sinks) {
+    const qift_status st = cache_shape(0, page_size, kv_heads, head_dim);
+    if (st != QIFT_OK) return st;
+    if (tokens < 0 || batch < 0 || max_q < 0 || max_pages < 0 || max_kv < 0 || prefix_len < 0 || window < 0 || sinks < 0)
+        return QIFT_ERR_INVALID_ARG;
+    if (q_heads <= 0 || q_heads % kv_heads != 0) return QIFT_ERR_INVALID_ARG;
+    const int64_t keys = (int64_t)max_pages * page_size + prefix_len;
+    if (keys > 1 << 30 || q_heads > 1 << 16 || tokens > (1LL << 40) / q_heads / head_dim) return QIFT_ERR_UNSUPPORTED;
+    a->tokens = tokens;
+    a->q_heads = q_heads;
+    a->kv_heads = kv_heads;
+    a->head_dim = head_dim;
+    a->batch = batch;
+    a->max_q = max_q;
+    a->log_page = log2_of(page_size);
+    a->max_pages = max_pages;
+    a->max_kv = max_kv > 0 && max_kv < keys ? max_kv : (int)keys;
+    a->prefix_len = prefix_len;
+    a->window = window;
+    a->sinks = sinks;
+    if (tokens > 0 && batch > 0 && max_q > 0 && !qift::attention_supported(*a)) return QIFT_ERR_UNSUPPORTED;
+    return QIFT_OK;
+}
+
 }  // namespace
 
 namespace qift {
@@ -254,6 +302,158 @@ qift_status qift_decode_linear(const void* x, int64_t tokens, int64_t n_in, int3
     return from_cuda(qift::launch_decode_linear(x, tokens, n_in, block, codes, w_scale, (int)set, n_out, y,
                                                 out_dt == QIFT_F16, q_out, act_scale_out,
                                                 static_cast<cudaStream_t>(stream)));
+}
+
+qift_status qift_append_kv(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                           const float* rope, int64_t rope_len, int32_t rope_dim, int32_t rope_interleaved,
+                           const int64_t* positions, const int64_t* slots, int32_t block, void* q_out,
+                           uint8_t* k_cache, float* k_scales, uint8_t* v_cache, float* v_scales, int64_t n_pages,
+                           int32_t page_size, void* stream) {
+    const qift_status st = cache_shape(n_pages, page_size, kv_heads, head_dim);
+    if (st != QIFT_OK) return st;
+    if (tokens < 0 || q_heads < 0 || (q == nullptr) != (q_heads == 0) || (q == nullptr) != (q_out == nullptr))
+        return QIFT_ERR_INVALID_ARG;
+    if (!head_block(block, head_dim)) return QIFT_ERR_INVALID_ARG;
+    if (rope && (rope_len < 0 || rope_dim <= 0 || rope_dim > head_dim || rope_dim % 2 != 0 ||
+                 (rope_interleaved != 0 && rope_interleaved != 1)))
+        return QIFT_ERR_INVALID_ARG;
+    if (rope && rope_dim % 16 != 0) return QIFT_ERR_UNSUPPORTED;
+    if (q_heads > 1 << 16 || tokens > 0x7fffffff / ((int64_t)q_heads + 2 * kv_heads)) return QIFT_ERR_UNSUPPORTED;
+    if (tokens == 0) return QIFT_OK;
+    if (!k || !v || !slots || (rope && !positions)) return QIFT_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) || !aligned4(v_scales) ||
+        !aligned8(slots) || !aligned8(positions))
+        return QIFT_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)q_heads * head_dim, kv_row = (int64_t)kv_heads * head_dim;
+    if ((q && (q_stride % 8 != 0 || q_stride < q_row)) || k_stride % 8 != 0 || k_stride < kv_row || v_stride % 8 != 0 ||
+        v_stride < kv_row)
+        return QIFT_ERR_INVALID_ARG;
+    const int64_t most = INT64_MAX / 4 / tokens;
+    if ((q && q_stride > most) || k_stride > most || v_stride > most) return QIFT_ERR_INVALID_ARG;
+    if (q) {
+        const int64_t out_bytes = tokens * q_row * 2;
+        if (overlap(q_out, out_bytes, q, ((tokens - 1) * q_stride + q_row) * 2) ||
+            overlap(q_out, out_bytes, k, ((tokens - 1) * k_stride + kv_row) * 2) ||
+            overlap(q_out, out_bytes, v, ((tokens - 1) * v_stride + kv_row) * 2))
+            return QIFT_ERR_INVALID_ARG;
+    }
+    qift::AppendArgs a = {};
+    a.q = static_cast<const __half*>(q);
+    a.k = static_cast<const __half*>(k);
+    a.v = static_cast<const __half*>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.rows = tokens * ((int64_t)q_heads + 2 * kv_heads);
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.rope = rope;
+    a.rope_len = rope_len;
+    a.rope_dim = rope_dim;
+    a.interleaved = rope_interleaved;
+    a.positions = positions;
+    a.slots = slots;
+    a.block = block;
+    a.q_out = static_cast<__half*>(q_out);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.n_pages = n_pages;
+    a.log_page = log2_of(page_size);
+    return from_cuda(qift::launch_append_kv(a, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const uint8_t* v_cache,
+                           const float* v_scales, int64_t n_pages, int32_t page_size, int32_t kv_heads,
+                           int32_t head_dim, const int64_t* slots, int64_t tokens, int32_t block, void* k_out,
+                           void* v_out, void* stream) {
+    const qift_status st = cache_shape(n_pages, page_size, kv_heads, head_dim);
+    if (st != QIFT_OK) return st;
+    if (tokens < 0 || !head_block(block, head_dim)) return QIFT_ERR_INVALID_ARG;
+    if (tokens > 0x7fffffff / (2 * (int64_t)kv_heads)) return QIFT_ERR_UNSUPPORTED;
+    if (tokens == 0) return QIFT_OK;
+    if (!slots || !k_out || !v_out) return QIFT_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) || !aligned4(v_scales) || !aligned8(slots) ||
+        !aligned16(k_out) || !aligned16(v_out))
+        return QIFT_ERR_INVALID_ARG;
+    qift::GatherArgs a = {};
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.rows = tokens * 2 * kv_heads;
+    a.n_pages = n_pages;
+    a.log_page = log2_of(page_size);
+    a.kv_heads = kv_heads;
+    a.slots = slots;
+    a.block = block;
+    a.k_out = static_cast<__half*>(k_out);
+    a.v_out = static_cast<__half*>(v_out);
+    return from_cuda(qift::launch_gather_kv(a, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t qift_paged_attention_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                       int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages,
+                                       int32_t max_kv, int32_t prefix_len, int32_t window, int32_t sinks) {
+    qift::AttentionArgs a = {};
+    if (attention_sizes(&a, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv, prefix_len,
+                        window, sinks) != QIFT_OK)
+        return -1;
+    return tokens == 0 || batch == 0 || max_q == 0 ? 0 : qift::attention_workspace_bytes(a);
+}
+
+qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, const int32_t* cu_q, int32_t batch, int32_t max_q,
+                                 const uint8_t* k_cache, const float* k_scales, const uint8_t* v_cache,
+                                 const float* v_scales, int64_t n_pages, int32_t page_size,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* kv_lens,
+                                 int32_t max_kv, const int32_t* prefix_table, int32_t prefix_len, int32_t window,
+                                 int32_t sinks, float scale, int32_t block, void* out, qift_dtype out_dt, float* lse,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+    if (out_dt != QIFT_F32 && out_dt != QIFT_F16) return QIFT_ERR_INVALID_ARG;
+    qift_status st = cache_shape(n_pages, page_size, kv_heads, head_dim);
+    if (st != QIFT_OK) return st;
+    qift::AttentionArgs a = {};
+    st = attention_sizes(&a, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv,
+                         prefix_len, window, sinks);
+    if (st != QIFT_OK) return st;
+    if (!head_block(block, head_dim) || !isfinite(scale)) return QIFT_ERR_INVALID_ARG;
+    if (!cu_q && tokens != (int64_t)batch * max_q) return QIFT_ERR_INVALID_ARG;
+    if (tokens == 0 || batch == 0 || max_q == 0) return QIFT_OK;
+    if (!q || !out || !kv_lens || (max_pages > 0 && !page_table) || (prefix_len > 0 && !prefix_table))
+        return QIFT_ERR_INVALID_ARG;
+    if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) ||
+        !aligned4(v_scales) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(page_table) ||
+        !aligned4(prefix_table) || !aligned4(lse) || !aligned16(workspace))
+        return QIFT_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || q_stride < (int64_t)q_heads * head_dim || q_stride > INT64_MAX / 4 / tokens)
+        return QIFT_ERR_INVALID_ARG;
+    const int64_t need = qift::attention_workspace_bytes(a);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return QIFT_ERR_INVALID_ARG;
+    a.q = static_cast<const __half*>(q);
+    a.q_stride = q_stride;
+    a.cu_q = cu_q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.n_pages = n_pages;
+    a.page_table = page_table;
+    a.kv_lens = kv_lens;
+    a.prefix_table = prefix_table;
+    a.scale_log2 = scale * 1.44269504089f;
+    a.block = block;
+    a.out = out;
+    a.f16 = out_dt == QIFT_F16;
+    a.lse = lse;
+    a.workspace = static_cast<float*>(workspace);
+    return from_cuda(qift::launch_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
 qift_status qift_device_error(void* stream, int32_t* detail) {

@@ -1,0 +1,595 @@
+// attention.cu -- qift_paged_attention: attention over the paged KV4 cache, for few rows a
+// sequence (decode), and the join of partial results.
+//
+// "Qift: Shift-Friendly No-Zero W2 Post-Training Quantization for Rotated W2A4/KV4 LLM
+// Inference" names KV4.  For a row (token at position p, query head) with the cache's rotated
+// codes k_j, v_j (whole numbers) and their scales s_j, t_j:
+//   u_j = scale * s_j * (q . k_j),   out = sum_j softmax(u)_j t_j v_j,   rotated back by H_b
+// over j <= p inside the window or among the sinks.  H_b is linear, so the rotation back is done
+// once on the result instead of once a key.
+//
+// The scores are formed transposed, S^T = K Q^T, on mma.sync m16n8k16: 16 keys by 8 rows.  A decode
+// step has few rows (the query heads of one kv head), so the keys take the wide side and half of
+// the products that 16 padded rows would cost are not made.  Codes go from shared memory to
+// fragments in registers: a lane takes a quarter of a key's row, and which product index a code
+// meets is free as long as Q is permuted alike.  Half of the codes are made exact halves
+// (1032 + c, minus 1032); the other half stay at c + 72 and the row's 72 * sum(q) is taken off
+// beforehand as the accumulator's start value, which saves one operation in nine.  P^T needs
+// tokens along its other axis: movmatrix transposes it 8 x 8.  V^T is the left operand of the
+// second product, its codes paired over two tokens by byte permutes, and exact.
+// Weights: t_j is multiplied into p_j before the rounding to binary16; the running reference is that
+// of u_j + log2 t_j, so the rounded weights lie in [0, 2^15] whatever the size of the values, and
+// keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace qift {
+namespace attn {
+
+constexpr int kWarps = 4;
+constexpr int kStep = 32;  // keys a warp takes at a time
+constexpr float kSlack = 7.0f, kLift = 8.0f;  // weights are at most 2^(kSlack + kLift) = 2^15 < 65504
+
+template <int D>
+struct Shape {
+    static constexpr int ROW = D / 2;                      // bytes of a key's codes
+    static constexpr int STAGE = 2 * kStep * ROW + 2 * kStep * 4;
+    static constexpr int STAGES = D == 256 ? 3 : 4;
+    static constexpr int KW = D / 32, VW = D / 64;         // 32-bit words of a key, of a value, a lane holds
+    static constexpr int MT = D / 16;                      // 16-high tiles of O^T
+    static constexpr int OPAD = D + 4;
+    static constexpr int ring_bytes() { return kWarps * STAGES * STAGE; }
+    static constexpr int join_bytes(int nr) { return kWarps * 8 * nr * (OPAD + 2) * 4; }
+    static constexpr int smem(int nr) { return std::max(ring_bytes(), join_bytes(nr)); }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two two's-complement nibbles, 16 bits apart, as binary16: from bits 0-3 exactly, from bits 4-7
+// plus 72 (1 x 2^6 with the nibble, its sign bit flipped, above the last four bits), or exactly.
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return sub2((w & 0x000F000Fu) ^ 0x64086408u, 0x64086408u); }
+__device__ __forceinline__ uint32_t nib_hi72(uint32_t w) { return (w & 0x00F000F0u) ^ 0x54805480u; }
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return sub2(nib_hi72(w), 0x54805480u); }
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], const uint8_t* p) {
+    if constexpr (BYTES == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    } else if constexpr (BYTES == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r[0] = v.x, r[1] = v.y;
+    } else {
+        r[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// How the blocks of a launch are dealt out: first the prefix's (row tile, kv head, split), then each
+// sequence's.  A split is a run of `*_chunk` steps of kStep keys.
+struct Deal {
+    int prefix_tiles, prefix_splits, prefix_chunk;
+    int own_tiles, own_splits, own_chunk;
+    int slots;  // partial results a row has room for; 0: one split and no prefix, rows are finished at once
+    int64_t blocks(int batch, int kv_heads) const {
+        return (int64_t)kv_heads * ((int64_t)prefix_tiles * prefix_splits + (int64_t)batch * own_tiles * own_splits);
+    }
+};
+
+// Eight query rows are the columns of one product tile; NR of them a block.
+template <int D, int NR>
+__global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs a, const Deal deal) {
+    using S = Shape<D>;
+    constexpr int R = 8 * NR;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t row_token[R];
+    __shared__ int row_pos[R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int G = a.q_heads / a.kv_heads;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // ---- which rows and keys
+    int64_t id = blockIdx.x;
+    const int64_t prefix_blocks = (int64_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
+    const bool prefix = id < prefix_blocks;
+    if (!prefix) id -= prefix_blocks;
+    const int splits = prefix ? deal.prefix_splits : deal.own_splits;
+    const int tiles = prefix ? deal.prefix_tiles : deal.own_tiles;
+    const int split = (int)(id % splits);
+    id /= splits;
+    const int h = (int)(id % a.kv_heads);
+    id /= a.kv_heads;
+    const int tile = (int)(id % tiles);
+    const int b = (int)(id / tiles);  // own only
+    const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
+    const int base = prefix ? 0 : a.prefix_len;
+    const int64_t capacity = prefix ? a.prefix_len : (int64_t)a.max_pages << a.log_page;
+    if (threadIdx.x < R) {
+        const int64_t r = (int64_t)tile * R + threadIdx.x;
+        int64_t token = -1;
+        int pos = -1;
+        if (prefix) {
+            if (r < a.tokens * G) token = r / G, pos = position_of(a, token);
+        } else {
+            const Sequence s = sequence(a, b);
+            if (r < (int64_t)s.q_len * G) {
+                token = s.first + r / G;
+                const int p = s.kv_len - s.q_len + (int)(r / G);
+                pos = p < 0 ? -1 : p;
+            }
+        }
+        if (token >= a.tokens || token < 0) token = -1;
+        row_token[threadIdx.x] = token;
+        row_pos[threadIdx.x] = pos;
+    }
+    __syncthreads();
+    int pmin = 0x7fffffff, pmax = -1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int p = row_pos[r];
+        if (p >= 0) pmin = min(pmin, p), pmax = max(pmax, p);
+    }
+    Range range = {0, 0, 0, 0};
+    if (pmax >= 0) range = visible<kStep>(a, pmin, pmax, base, capacity);
+    // The host's chunk covers lengths up to its bound; a longer sequence takes longer splits.
+    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
+    const int s_begin = min(split * chunk, range.steps), s_end = min(s_begin + chunk, range.steps);
+
+    // ---- this lane's rows: column g of a tile as a right operand, columns 2t and 2t + 1 as a result
+    uint32_t qf[NR][S::KW][4];
+    float start[NR][2];
+    int pos[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int64_t token = row_token[8 * n + g];
+        const int head = h * G + (int)(((int64_t)tile * R + 8 * n + g) % G);
+        float odd = 0.0f;
+#pragma unroll
+        for (int w = 0; w < S::KW; ++w) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            const int d = (w / 4) * 128 + (D >= 128 ? 32 : 16) * t + 8 * (w % 4);
+            if (token >= 0) x = *reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (int64_t)head * D + d);
+            qf[n][w][0] = prmt(x.x, x.z, 0x5410u);  // values 0, 4 of the eight that meet a word's nibbles
+            qf[n][w][1] = prmt(x.x, x.z, 0x7632u);  // 1, 5
+            qf[n][w][2] = prmt(x.y, x.w, 0x5410u);  // 2, 6
+            qf[n][w][3] = prmt(x.y, x.w, 0x7632u);  // 3, 7
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[n][w][1]));
+            const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&qf[n][w][3]));
+            odd += (f.x + f.y) + (e.x + e.y);
+        }
+        odd += __shfl_xor_sync(0xffffffffu, odd, 1);
+        odd += __shfl_xor_sync(0xffffffffu, odd, 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            start[n][c] = -72.0f * __shfl_sync(0xffffffffu, odd, (2 * t + c) * 4);
+            pos[n][c] = row_pos[8 * n + 2 * t + c];
+        }
+    }
+
+    float o[NR][S::MT][4];
+    float ref[NR][2], sum[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+        for (int m = 0; m < S::MT; ++m)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[n][m][c] = 0.0f;
+        ref[n][0] = ref[n][1] = kNone;
+        sum[n][0] = sum[n][1] = 0.0f;
+    }
+
+    // ---- the ring of this warp: lanes 0-15 copy the first 16 keys of a step, lanes 16-31 the rest
+    uint8_t* ring = smem + warp * (S::STAGES * S::STAGE);
+    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const int half = lane >> 4, l16 = lane & 15;
+    const int page_mask = (1 << a.log_page) - 1;
+    // Page of this lane's half of a step, -1 where there is none.
+    auto page_of = [&](int s) -> int {
+        if (s >= s_end) return -1;
+        const int j = range.block(s) * kStep + half * 16;
+        if (j >= range.limit) return -1;
+        const int p = table[j >> a.log_page];
+        return (uint32_t)p < (uint64_t)a.n_pages ? p : -1;
+    };
+    auto issue = [&](int s, int stage, int page) {
+        if (page >= 0) {
+            const int off = (range.block(s) * kStep + half * 16) & page_mask;
+            const int64_t at = (((int64_t)page * a.kv_heads + h) << a.log_page) + off;
+            if (QIFT_CK_RANGE(at, 16, (a.n_pages * a.kv_heads) << a.log_page)) {
+                const uint8_t* ks = a.k_cache + at * S::ROW;
+                const uint8_t* vs = a.v_cache + at * S::ROW;
+                const uint32_t dst = ring32 + stage * S::STAGE + half * 16 * S::ROW;
+                constexpr int CH = S::ROW / 16;  // 16-byte pieces of a row
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int tok = (l16 + 16 * i) / CH, c = (l16 + 16 * i) % CH;
+                    // Keys lie in the order of the product's rows (row r is key (r & 8) + (r & 1) * 4 +
+                    // (r & 7) / 2); pieces are swapped so that the lanes' reads meet no bank twice.
+                    const int r = (tok & 8) | ((tok & 3) << 1) | ((tok >> 2) & 1);
+                    const int kc = D == 256 ? c ^ ((r & 1) * 4) : c;
+                    const int vc = D == 256 ? c ^ ((tok & 3) * 2) : D == 128 ? c ^ (((tok >> 1) & 1) * 2) : c;
+                    cp16(dst + r * S::ROW + kc * 16, ks + (l16 + 16 * i) * 16);
+                    cp16(dst + kStep * S::ROW + tok * S::ROW + vc * 16, vs + (l16 + 16 * i) * 16);
+                }
+                const uint32_t sc = ring32 + stage * S::STAGE + 2 * kStep * S::ROW + lane * 4;
+                cp4(sc, a.k_scales + at + l16);
+                cp4(sc + kStep * 4, a.v_scales + at + l16);
+            }
+        }
+        cp_commit();
+    };
+
+    int page_next = page_of(s_begin + warp);
+    uint32_t there = 0;  // per stage two bits: which halves of the step hold keys
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; ++i) {
+        const int s = s_begin + warp + i * kWarps;
+        const int page = page_next;
+        page_next = page_of(s + kWarps);
+        const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+        there |= ((ok & 1u) | ((ok >> 15) & 2u)) << (2 * i);
+        issue(s, i, page);
+    }
+    int stage = 0;
+    for (int s = s_begin + warp; s < s_end; s += kWarps) {
+        {
+            const int sn = s + (S::STAGES - 1) * kWarps;
+            const int st = stage == 0 ? S::STAGES - 1 : stage - 1;
+            const int page = page_next;
+            page_next = page_of(sn + kWarps);
+            const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);  // every lane is past its reads of that stage
+            there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 15) & 2u)) << (2 * st));
+            issue(sn, st, page);
+        }
+        cp_wait<S::STAGES - 1>();
+        __syncwarp();
+        const uint8_t* st = ring + stage * S::STAGE;
+        const float* scales = reinterpret_cast<const float*>(st + 2 * kStep * S::ROW);
+        const int j0 = base + range.block(s) * kStep;  // position of the step's first key
+        const uint32_t has = (there >> (2 * stage)) & 3u;
+        const bool all = has == 3u && j0 + kStep - 1 <= pmin && (!a.window || j0 > pmax - a.window || j0 + kStep <= a.sinks) &&
+                         j0 - base + kStep <= range.limit;
+
+        // ---- scores, in log2 units
+        float x[2][NR][4], vs[2][2], lv[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int row = c * 16 + (g & 1) * 4 + (g >> 1);  // key of product row g; row g + 8 is 8 further
+            float ks[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                ks[e] = scales[row + 8 * e] * a.scale_log2;
+                vs[c][e] = scales[kStep + row + 8 * e];
+                lv[c][e] = fmaxf(lg2(vs[c][e]), -28.0f);  // the smallest scale is 2^-24 / 7
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                x[c][n][0] = x[c][n][2] = start[n][0];
+                x[c][n][1] = x[c][n][3] = start[n][1];
+            }
+            constexpr int KB = D >= 128 ? 16 : 8;  // bytes a read takes
+#pragma unroll
+            for (int i = 0; i < S::KW * 4 / KB; ++i) {
+                uint32_t w0[KB / 4], w1[KB / 4];
+                const int at = D == 256 ? ((4 * i + t) ^ ((g & 1) * 4)) * 16 : t * KB;
+                lds<KB>(w0, st + (c * 16 + g) * S::ROW + at);
+                lds<KB>(w1, st + (c * 16 + g + 8) * S::ROW + at);
+#pragma unroll
+                for (int w = 0; w < KB / 4; ++w) {
+                    const int k = i * (KB / 4) + w;
+                    uint32_t a0 = w0[w], a1 = w1[w];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t l0 = nib_lo(a0), l1 = nib_lo(a1), h0 = nib_hi72(a0), h1 = nib_hi72(a1);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma16816(x[c][n], l0, l1, h0, h1, qf[n][k][2 * e], qf[n][k][2 * e + 1]);
+                        a0 >>= 8, a1 >>= 8;
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                x[c][n][0] *= ks[0], x[c][n][1] *= ks[0];
+                x[c][n][2] *= ks[1], x[c][n][3] *= ks[1];
+            }
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = j0 + row + 8 * e;
+                    const bool in = ((has >> c) & 1u) && j - base < range.limit;
+                    bool any = false;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int p = pos[n][q];
+                            const bool see = in && j <= p && (!a.window || j > p - a.window || j < a.sinks);
+                            if (!see) x[c][n][2 * e + q] = -INFINITY;
+                            any |= see;
+                        }
+                    // What no row sees may hold anything: its scale must not reach the sums.
+                    if (!any) vs[c][e] = 0.0f, lv[c][e] = -28.0f;
+                }
+            }
+        }
+
+        // ---- the reference: raised, and what is summed so far scaled down, only where a weight would
+        // pass 2^(kSlack + kLift); the same for every lane of a row, so a vote decides
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float top[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                top[q] = fmaxf(fmaxf(x[0][n][q] + lv[0][0], x[0][n][2 + q] + lv[0][1]),
+                               fmaxf(x[1][n][q] + lv[1][0], x[1][n][2 + q] + lv[1][1]));
+            if (__any_sync(0xffffffffu, top[0] > ref[n][0] + kSlack || top[1] > ref[n][1] + kSlack)) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], m));
+                    const float to = fmaxf(ref[n][q], top[q]);
+                    const float down = ex2(ref[n][q] - to);
+                    ref[n][q] = to;
+                    sum[n][q] *= down;
+#pragma unroll
+                    for (int m = 0; m < S::MT; ++m) o[n][m][q] *= down, o[n][m][2 + q] *= down;
+                }
+            }
+        }
+
+        // ---- weights and the second product
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t p[NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w0 = ex2(x[c][n][2 * e] - (ref[n][0] - kLift));
+                    const float w1 = ex2(x[c][n][2 * e + 1] - (ref[n][1] - kLift));
+                    sum[n][0] += w0;
+                    sum[n][1] += w1;
+                    const __half2 h2 = __floats2half2_rn(w0 * vs[c][e], w1 * vs[c][e]);
+                    p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h2));
+                }
+            constexpr int VB = S::VW * 4;
+            uint32_t v[4][S::VW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tok = t + 4 * i;  // product indexes 2t, 2t + 1, 2t + 8, 2t + 9
+                const int at = D == 256   ? (g ^ ((tok & 3) * 2)) * 16
+                               : D == 128 ? ((g >> 1) ^ (((tok >> 1) & 1) * 2)) * 16 + (g & 1) * 8
+                                          : g * 4;
+                lds<VB>(v[i], st + kStep * S::ROW + (c * 16 + tok) * S::ROW + at);
+            }
+#pragma unroll
+            for (int w = 0; w < S::VW; ++w)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t lo = prmt(v[0][w], v[1][w], u ? 0x7632u : 0x5410u);
+                    uint32_t hi = prmt(v[2][w], v[3][w], u ? 0x7632u : 0x5410u);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a0 = nib_lo(lo), a1 = nib_hi(lo), a2 = nib_lo(hi), a3 = nib_hi(hi);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma16816(o[n][w * 4 + u * 2 + e], a0, a1, a2, a3, p[n][0], p[n][1]);
+                        lo >>= 8, hi >>= 8;
+                    }
+                }
+        }
+        __syncwarp();
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // ---- join the warps.  Lane (g, t) holds values g * D/8 + 0 .. D/8 - 1 of rows 2t, 2t + 1.
+    float* po = reinterpret_cast<float*>(smem);
+    float* pm = po + kWarps * R * S::OPAD;
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int m = 4; m < 32; m <<= 1) sum[n][q] += __shfl_xor_sync(0xffffffffu, sum[n][q], m);
+            const int r = 8 * n + 2 * t + q;
+            float* dst = po + (warp * R + r) * S::OPAD + g * (D / 8);
+#pragma unroll
+            for (int m = 0; m < S::MT; m += 2)
+                *reinterpret_cast<float4*>(dst + 2 * m) =
+                    make_float4(o[n][m][q], o[n][m][2 + q], o[n][m + 1][q], o[n][m + 1][2 + q]);
+            if (g == 0) {
+                pm[(warp * R + r) * 2] = ref[n][q];
+                pm[(warp * R + r) * 2 + 1] = sum[n][q];
+            }
+        }
+    __syncthreads();
+    constexpr int E = D / 32;
+    for (int r = warp; r < R; r += kWarps) {
+        const int64_t token = row_token[r];
+        if (token < 0) continue;
+        const int head = h * G + (int)(((int64_t)tile * R + r) % G);
+        float M = kNone, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pm[(w * R + r) * 2]);
+        float acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(pm[(w * R + r) * 2] - M);
+            L += f * pm[(w * R + r) * 2 + 1];
+            const float* src = po + (w * R + r) * S::OPAD + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] += f * src[i];
+        }
+        M -= kLift;
+        if (deal.slots == 0) {
+            finish_row<D>(a, acc, M, L, token, head, lane);
+        } else {
+            const Parts p = parts(a, deal.slots);
+            const int64_t at = (token * a.q_heads + head) * deal.slots + (prefix ? split : deal.prefix_splits + split);
+            if (lane == 0) p.ml[at] = make_float2(M, L);
+            if (L > 0.0f) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) p.o[at * D + lane * E + i] = acc[i];
+            }
+        }
+    }
+}
+
+// Joins the partial results of a row: one warp a row, rows dealt out as (sequence, token, head).
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const AttentionArgs a, const int slots) {
+    constexpr int E = D / 32;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int head = (int)(row % a.q_heads);
+    row /= a.q_heads;
+    const int i = (int)(row % a.max_q);
+    const int64_t b = row / a.max_q;
+    if (b >= a.batch) return;
+    const Sequence s = sequence(a, (int)b);
+    if (i >= s.q_len) return;
+    const int64_t token = s.first + i;
+    const Parts p = parts(a, slots);
+    const int64_t at = (token * a.q_heads + head) * slots;
+    float M = kNone;
+    for (int k = lane; k < slots; k += 32) M = fmaxf(M, p.ml[at + k].x);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    float L = 0.0f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int k = 0; k < slots; ++k) {
+        const float2 ml = p.ml[at + k];
+        if (!(ml.y > 0.0f)) continue;
+        const float f = ex2(ml.x - M);
+        L += f * ml.y;
+        const float* src = p.o + (at + k) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+    }
+    finish_row<D>(a, acc, M, L, token, head, lane);
+}
+
+static Deal deal_out(const AttentionArgs& a, int rows) {
+    const int G = a.q_heads / a.kv_heads;
+    Deal d = {};
+    d.own_tiles = (int)(((int64_t)a.max_q * G + rows - 1) / rows);
+    // Blocks enough for four turns of every SM's room, but no split under 512 keys (four steps a warp).
+    const int64_t want = 148 * 3 * 4, least = 16;
+    auto split = [&](int64_t blocks, int64_t keys, int* splits, int* chunk) {
+        const int64_t steps = (keys + kStep - 1) / kStep + 1;
+        int64_t n = (want + blocks - 1) / blocks;
+        n = std::max<int64_t>(1, std::min(n, steps / least));
+        *chunk = (int)((steps + n - 1) / n);
+        *splits = (int)((steps + *chunk - 1) / *chunk);
+    };
+    int64_t own = (int64_t)a.max_kv - a.prefix_len;
+    int64_t shared = a.prefix_len;
+    if (a.window) {
+        const int64_t most = (int64_t)a.window + a.max_q + a.sinks + 2 * kStep;
+        own = std::min(own, most);
+        // rows of the whole batch stand at positions far apart: no bound on what they see of the prefix
+    }
+    own = std::max<int64_t>(own, 1);
+    split((int64_t)a.batch * a.kv_heads * d.own_tiles, own, &d.own_splits, &d.own_chunk);
+    if (a.prefix_len) {
+        d.prefix_tiles = (int)((a.tokens * G + rows - 1) / rows);
+        split((int64_t)a.kv_heads * d.prefix_tiles, shared, &d.prefix_splits, &d.prefix_chunk);
+    }
+    d.slots = a.prefix_len || d.own_splits > 1 ? d.prefix_splits + d.own_splits : 0;
+    return d;
+}
+
+template <int D, int NR>
+static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
+    const size_t smem = Shape<D>::smem(NR);
+    cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)d.blocks(a.batch, a.kv_heads));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, stream_kernel<D, NR>, a, d);
+    if (e != cudaSuccess || d.slots == 0) return e;
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.batch * a.max_q * a.q_heads + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, d.slots);
+}
+
+static int rows_per_block(const AttentionArgs& a) {
+    const int64_t G = a.q_heads / a.kv_heads;
+    const int64_t rows = std::max<int64_t>((int64_t)a.max_q * G, a.prefix_len ? a.tokens * G : 0);
+    return rows <= 8 ? 8 : 16;
+}
+
+template <int D>
+static cudaError_t launch_rows_of(const AttentionArgs& a, cudaStream_t s) {
+    const int rows = rows_per_block(a);
+    const Deal d = deal_out(a, rows);
+    return rows == 8 ? launch_stream<D, 1>(a, d, s) : launch_stream<D, 2>(a, d, s);
+}
+
+}  // namespace attn
+
+bool attention_supported(const AttentionArgs& a) {
+    const attn::Deal d = attn::deal_out(a, attn::rows_per_block(a));
+    return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads / 8 < 0x7fffffff;
+}
+
+int64_t attention_workspace_bytes(const AttentionArgs& a) {
+    const attn::Deal d = attn::deal_out(a, attn::rows_per_block(a));
+    return a.tokens * a.q_heads * d.slots * (a.head_dim + 2) * 4;
+}
+
+cudaError_t launch_attention(AttentionArgs a, cudaStream_t s) {
+    a.norm = a.block ? (float)(1.0 / sqrt((double)a.block)) : 1.0f;
+    switch (a.head_dim) {
+        case 64: return attn::launch_rows_of<64>(a, s);
+        case 128: return attn::launch_rows_of<128>(a, s);
+        case 256: return attn::launch_rows_of<256>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace qift

@@ -1,0 +1,186 @@
+// attention.cuh -- what the kernels of qift_paged_attention share: which rows a block owns, which
+// keys they see, and how partial results are laid down and joined.
+//
+// A row is one (token, query head).  Rows that share a kv head are handled together: row r of a
+// row set is token r / G, head r % G of the group (G = q_heads / kv_heads).  Two kinds of row set:
+//   own     the tokens of one sequence, against that sequence's own pages
+//   prefix  the tokens of the whole batch, against the pages every sequence starts with, so that
+//           those keys are read once for all
+// Key positions count from the start of the sequence; the own pages hold positions prefix_len, ...
+//
+// Partial results of a row over a set S of keys, with u_j = scale log2(e) q.k_j:
+//   M, L = sum_S 2^(u_j - M), O = sum_S 2^(u_j - M) v_j
+// and any number of them join by M* = max M, L* = sum L 2^(M - M*), O* likewise.  An empty set has
+// M = kNone, L = 0.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace qift {
+namespace attn {
+
+constexpr int kMaxKeys = 1 << 30;  // of a sequence, so that positions plus a block stay in 32 bits
+constexpr float kNone = -1e30f;  // finite, so that the difference of two of them is a number
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One sequence as the device sees it; offsets and lengths that contradict the call's sizes are cut
+// so that no index leaves the caller's arrays.
+struct Sequence {
+    int64_t first;  // first token
+    int q_len, kv_len;
+};
+__device__ __forceinline__ Sequence sequence(const AttentionArgs& a, int b) {
+    Sequence s;
+    if (a.cu_q) {
+        int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
+        lo = lo < 0 ? 0 : lo;
+        hi = hi > a.tokens ? a.tokens : hi;
+        s.first = lo;
+        s.q_len = hi > lo ? (int)(hi - lo) : 0;
+        if (s.q_len > a.max_q) s.q_len = a.max_q;
+    } else {
+        s.first = (int64_t)b * a.max_q;
+        s.q_len = a.max_q;
+    }
+    const int n = a.kv_lens[b];
+    s.kv_len = n < 0 ? 0 : n > kMaxKeys ? kMaxKeys : n;
+    return s;
+}
+
+// The sequence a token belongs to, -1 if none: the last b with cu_q[b] <= token < cu_q[b + 1].
+__device__ __forceinline__ int sequence_of(const AttentionArgs& a, int64_t token) {
+    if (!a.cu_q) return (int)(token / a.max_q);
+    int lo = 0, hi = a.batch;  // first b in [lo, hi] with cu_q[b] > token
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_q[mid] > token) hi = mid;
+        else lo = mid + 1;
+    }
+    const int b = lo - 1;
+    return b >= 0 && token < a.cu_q[b + 1] ? b : -1;
+}
+
+// Position of a token in its sequence, or -1 (it sees nothing).
+__device__ __forceinline__ int position_of(const AttentionArgs& a, int64_t token) {
+    const int b = sequence_of(a, token);
+    if (b < 0) return -1;
+    const Sequence s = sequence(a, b);
+    const int64_t p = (int64_t)s.kv_len - s.q_len + (token - s.first);
+    return p < 0 ? -1 : (int)p;
+}
+
+// The blocks of STEP keys that rows at positions [pmin, pmax] can see, of a table that holds
+// positions [base, base + capacity): first those that hold sinks, then those of the window.
+// Step s is key block s (s < head) or s - head + main; keys at table index >= limit do not exist.
+struct Range {
+    int head, main, steps, limit;
+    __device__ __forceinline__ int block(int s) const { return s < head ? s : main + (s - head); }
+};
+template <int STEP>
+__device__ __forceinline__ Range visible(const AttentionArgs& a, int pmin, int pmax, int base, int64_t capacity) {
+    Range r;
+    int64_t hi = (int64_t)pmax + 1 - base;
+    if (hi > capacity) hi = capacity;
+    if (hi < 0) hi = 0;
+    int64_t lo = a.window ? (int64_t)pmin - a.window + 1 : 0;
+    if (lo < 0) lo = 0;
+    int64_t sinks = lo < a.sinks ? lo : a.sinks;  // sinks in front of the window
+    sinks -= base;
+    if (sinks < 0) sinks = 0;
+    if (sinks > hi) sinks = hi;
+    lo -= base;
+    if (lo < 0) lo = 0;
+    r.limit = (int)hi;
+    r.head = (int)((sinks + STEP - 1) / STEP);
+    int64_t m = lo / STEP;
+    if (m < r.head) m = r.head;
+    const int64_t end = (hi + STEP - 1) / STEP;
+    r.main = (int)m;
+    r.steps = r.head + (end > m ? (int)(end - m) : 0);
+    return r;
+}
+
+// Partial results: slot p of row (token, head): D floats of O and (M, L).
+struct Parts {
+    float* o;
+    float2* ml;
+    int slots;
+};
+__host__ __device__ inline Parts parts(const AttentionArgs& a, int slots) {
+    Parts p;
+    p.o = a.workspace;
+    p.ml = reinterpret_cast<float2*>(a.workspace + (int64_t)a.tokens * a.q_heads * slots * a.head_dim);
+    p.slots = slots;
+    return p;
+}
+
+// Rotates a row held by a warp, D / 32 contiguous values a lane, by blocks of `block` (0: not).
+template <int D>
+__device__ __forceinline__ void row_hadamard(float (&v)[D / 32], int lane, int block, float norm) {
+    if (block == 0) return;
+    constexpr int E = D / 32;
+#pragma unroll
+    for (int h = 1; h < E; h <<= 1) {
+        if (block <= h) break;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (i & h) continue;
+            const float x = v[i], y = v[i + h];
+            v[i] = x + y;
+            v[i + h] = x - y;
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        if (block <= E * m) break;
+        const float sgn = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = __fmaf_rn(sgn, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] *= norm;
+}
+
+// Normalise, rotate back, round once and store a finished row (a warp's).  M, L as above.
+template <int D>
+__device__ __forceinline__ void finish_row(const AttentionArgs& a, float (&v)[D / 32], float M, float L, int64_t token,
+                                           int head, int lane) {
+    constexpr int E = D / 32;
+    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] *= inv;
+    row_hadamard<D>(v, lane, a.block, a.norm);
+    const int64_t at = (token * a.q_heads + head) * D + lane * E;
+    if (a.f16) {
+        __half2 h[E / 2];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        __half* o = static_cast<__half*>(a.out) + at;
+        if constexpr (E == 2) *reinterpret_cast<__half2*>(o) = h[0];
+        else if constexpr (E == 4) *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(h);
+        else *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(h);
+    } else {
+        float* o = static_cast<float*>(a.out) + at;
+        if constexpr (E == 2) *reinterpret_cast<float2*>(o) = make_float2(v[0], v[1]);
+        else
+#pragma unroll
+            for (int i = 0; i < E; i += 4)
+                *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    if (a.lse && lane == 0)
+        a.lse[token * a.q_heads + head] = L > 0.0f ? 0.69314718056f * (M + log2f(L)) : -INFINITY;
+}
+
+}  // namespace attn
+}  // namespace qift

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -100,6 +101,68 @@ cudaError_t read_and_clear_one_token_error(int* word);
 bool linear_w4_supported(int64_t tokens, int64_t n_in);
 cudaError_t launch_linear_w4(const int8_t* q, const float* s_a, const uint32_t* codes, const float* s_w,
                              int64_t tokens, int64_t n_out, int64_t n_in, void* y, bool f16, cudaStream_t s);
+
+// Paged KV4 cache (qift_append_kv, qift_gather_kv).  rows = tokens * heads handled, one row of head_dim
+// values each; the launchers fill in `norm`.
+struct AppendArgs {
+    const __half *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int64_t rows;
+    int q_heads, kv_heads;                 // q_heads 0: no queries
+    const float* rope;                     // [rope_len][rope_dim], or null: no position rotation
+    int64_t rope_len;
+    int rope_dim, interleaved;
+    const int64_t *positions, *slots;
+    int block;
+    float norm;
+    __half* q_out;
+    uint8_t *k_cache, *v_cache;
+    float *k_scales, *v_scales;
+    int64_t n_pages;
+    int log_page;
+};
+struct GatherArgs {
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    int64_t rows, n_pages;
+    int log_page, kv_heads;
+    const int64_t* slots;
+    int block;
+    float norm;
+    __half *k_out, *v_out;
+};
+cudaError_t launch_append_kv(AppendArgs a, int head_dim, cudaStream_t s);
+cudaError_t launch_gather_kv(GatherArgs a, int head_dim, cudaStream_t s);
+
+// Attention over the paged KV4 cache (qift_paged_attention).
+struct AttentionArgs {
+    const __half* q;
+    int64_t q_stride, tokens;
+    int q_heads, kv_heads, head_dim;
+    const int32_t* cu_q;  // null: every sequence has max_q tokens
+    int batch, max_q;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    int64_t n_pages;
+    int log_page;
+    const int32_t* page_table;  // [batch][max_pages]
+    int max_pages;
+    const int32_t* kv_lens;     // [batch], the prefix included
+    int max_kv;                 // host's bound on kv_lens: sizes the split, not the result
+    const int32_t* prefix_table;
+    int prefix_len;
+    int window, sinks;          // window 0: none
+    float scale_log2;           // softmax scale times log2(e)
+    int block;
+    float norm;
+    void* out;
+    bool f16;
+    float* lse;                 // [tokens][q_heads] or null
+    float* workspace;
+};
+bool attention_supported(const AttentionArgs& a);
+int64_t attention_workspace_bytes(const AttentionArgs& a);
+cudaError_t launch_attention(AttentionArgs a, cudaStream_t s);
 
 // Test hooks behind qift_debug.h (numbers 3 to 5 named GEMM forms that are no longer built).
 enum LinearPath {
