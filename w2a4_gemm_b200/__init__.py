@@ -13,6 +13,7 @@ these functions raise.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 
@@ -349,52 +350,65 @@ def qift_decode_linear(x: torch.Tensor, block: int, codes: torch.Tensor, w_scale
     return y
 
 
-def _head_rows(t: torch.Tensor, name: str) -> int:
-    """Checks a [tokens, heads, head_dim] fp16 tensor whose heads lie one behind the other (a slice of a
-    projection's output is one); returns the elements between tokens."""
+# The paged cache's calls are made once a layer and token, so their checks are kept lean: one quick test a
+# tensor, and the checks above only to say what is wrong.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _is(t, name: str, dtype, shape: tuple, index: int) -> int:
+    """Address of `t`, which must be a contiguous tensor of this dtype and shape on CUDA device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _shape(_cuda(t, name, dtype), name, shape)
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{index}")
+
+
+def _heads(t, name: str, shape: tuple, index: int) -> tuple[int, int]:
+    """Address and elements between tokens of a [tokens, heads, head_dim] fp16 tensor whose heads lie one behind
+    the other (a slice of a projection's output is one)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got shape {tuple(t.shape)}")
-    n, h, d = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{index}")
+    n, h, d = shape
     row, head, one = t.stride()
     if n <= 1:
         row = h * d
     if (one != 1 and d > 1) or (head != d and h > 1) or row < h * d:
         raise ValueError(f"{name} must hold each token's heads one behind the other, got strides {t.stride()}")
-    return row
+    return t.data_ptr(), row
 
 
 def _cache(k_cache, k_scales, v_cache, v_scales):
-    """Checks a paged cache; returns (pages, kv_heads, page_size, head_dim)."""
+    """Checks a paged cache; returns its addresses, (pages, kv_heads, page_size, head_dim) and its device's index."""
     _cuda(k_cache, "k_cache", torch.uint8)
-    _cuda(v_cache, "v_cache", torch.uint8)
-    _cuda(k_scales, "k_scales", torch.float32)
-    _cuda(v_scales, "v_scales", torch.float32)
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim / 2], got shape {tuple(k_cache.shape)}")
-    _shape(v_cache, "v_cache", k_cache.shape)
-    _shape(k_scales, "k_scales", k_cache.shape[:3])
-    _shape(v_scales, "v_scales", k_cache.shape[:3])
-    pages, heads, size, half = k_cache.shape
-    return pages, heads, size, 2 * half
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim / 2], got shape {tuple(shape)}")
+    index, of_scales = k_cache.get_device(), shape[:3]
+    at = (k_cache.data_ptr(), _is(k_scales, "k_scales", torch.float32, of_scales, index),
+          _is(v_cache, "v_cache", torch.uint8, shape, index), _is(v_scales, "v_scales", torch.float32, of_scales, index))
+    return at, (shape[0], shape[1], shape[2], 2 * shape[3]), index
 
 
-class _on:
-    """Makes `dev` the current device for a launch; nothing where it is already."""
-
-    def __init__(self, dev):
-        self.other = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-
-    def __exit__(self, *e):
-        if self.other is not None:
-            self.other.__exit__(*e)
+def _launch(index: int, stream, fn, *args) -> int:
+    """Calls the library's `fn` on `stream` (None: the current one of device `index`) with that device current."""
+    if stream is None:
+        stream = _current_stream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        return fn(*args, stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream)
 
 
 def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block: int, k_cache: torch.Tensor,
@@ -409,39 +423,35 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
     fp32 ``[pages, kv_heads, page_size]`` are written at ``slots`` (int64, ``page * page_size + offset``; -1 =
     padding).  ``rope`` fp32 ``[positions, rope_dim]`` holds cosines, then sines, and ``positions`` (int64) its row
     for each token.  Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
-    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    ks, vs = _head_rows(k, "k"), _head_rows(v, "v")
-    T = k.shape[0]
-    _shape(k, "k", (T, kv_heads, d))
-    _shape(v, "v", (T, kv_heads, d))
-    _shape(_cuda(slots, "slots", torch.int64), "slots", (T,))
-    qs = hq = 0
-    if q is not None:
-        qs, hq = _head_rows(q, "q"), q.shape[1]
-        _shape(q, "q", (T, hq, d))
-        if q_out is not None:
-            _shape(_cuda(q_out, "q_out", torch.float16), "q_out", (T, hq, d))
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rope_len = rope_dim = 0
+    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
+    k_at, k_row = _heads(k, "k", (T, kv_heads, d), index)
+    v_at, v_row = _heads(v, "v", (T, kv_heads, d), index)
+    slots_at = _is(slots, "slots", torch.int64, (T,), index)
+    q_at = out_at = rope_at = positions_at = None
+    q_row = hq = rope_len = rope_dim = 0
     if rope is not None:
-        rope_len, rope_dim = _2d(_cuda(rope, "rope", torch.float32), "rope").shape
         if positions is None:
             raise ValueError("rope needs positions")
-        _shape(_cuda(positions, "positions", torch.int64), "positions", (T,))
-    dev = _same_device(("k", k), ("v", v), ("slots", slots), ("k_cache", k_cache), ("k_scales", k_scales),
-                       ("v_cache", v_cache), ("v_scales", v_scales), ("q", q), ("q_out", q_out), ("rope", rope),
-                       ("positions", positions if rope is not None else None))
-    if q is not None and hq == 0:
-        raise ValueError("q must have at least one head")
-    if q is not None and q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=torch.float16, device=dev)
-    with _on(dev):
-        _check(lib().qift_append_kv(_ptr(q) if T else None, qs, _ptr(k), ks, _ptr(v), vs, T, hq if T else 0, kv_heads, d,
-                                    _ptr(rope) if T else None, rope_len, rope_dim, 1 if interleaved else 0,
-                                    _ptr(positions) if rope is not None else None, _ptr(slots), block,
-                                    _ptr(q_out) if T else None, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
-                                    _ptr(v_scales), pages, size, _stream(stream, dev)), "qift_append_kv")
+        rope_len, rope_dim = _2d(_cuda(rope, "rope", torch.float32), "rope").shape
+        rope_at = _is(rope, "rope", torch.float32, (rope_len, rope_dim), index)
+        positions_at = _is(positions, "positions", torch.int64, (T,), index)
+    if q is not None:
+        hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        q_at, q_row = _heads(q, "q", (T, hq, d), index)
+        if hq == 0:
+            raise ValueError("q must have at least one head")
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=torch.float16, device=k.device)
+            out_at = q_out.data_ptr()
+        else:
+            out_at = _is(q_out, "q_out", torch.float16, (T, hq, d), index)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if T:  # an empty tensor has no address
+        _check(_launch(index, stream, lib().qift_append_kv, q_at, q_row, k_at, k_row, v_at, v_row, T, hq, kv_heads, d,
+                       rope_at, rope_len, rope_dim, 1 if interleaved else 0, positions_at, slots_at, block, out_at, kc,
+                       ks, vc, vs, pages, size), "qift_append_kv")
     return q_out
 
 
@@ -449,18 +459,13 @@ def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch
                    slots: torch.Tensor, block: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows of a paged KV4 cache read back, rotated back by ``block`` (0: in the cache's domain): fp16
     ``(k, v)``, each ``[tokens, kv_heads, head_dim]``; zeros for slots outside the cache."""
-    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    _cuda(slots, "slots", torch.int64)
-    if slots.dim() != 1:
-        raise ValueError(f"slots must be 1-D, got shape {tuple(slots.shape)}")
-    T = slots.shape[0]
-    dev = _same_device(("k_cache", k_cache), ("k_scales", k_scales), ("v_cache", v_cache), ("v_scales", v_scales),
-                       ("slots", slots))
-    k, v = torch.empty((2, T, kv_heads, d), dtype=torch.float16, device=dev).unbind(0)
-    with _on(dev):
-        _check(lib().qift_gather_kv(_ptr(k_cache), _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), pages, size, kv_heads,
-                                    d, _ptr(slots), T, block, _ptr(k), _ptr(v), _stream(stream, dev)),
-               "qift_gather_kv")
+    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() else 0
+    slots_at = _is(slots, "slots", torch.int64, (T,), index)
+    k = torch.empty((T, kv_heads, d), dtype=torch.float16, device=slots.device)
+    v = torch.empty((T, kv_heads, d), dtype=torch.float16, device=slots.device)
+    _check(_launch(index, stream, lib().qift_gather_kv, kc, ks, vc, vs, pages, size, kv_heads, d, slots_at, T, block,
+                   k.data_ptr(), v.data_ptr()), "qift_gather_kv")
     return k, v
 
 
@@ -482,59 +487,66 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     0 takes it).  ``lse`` (fp32 ``[tokens, q_heads]``), if given, receives the log-sum-exp.  ``workspace`` (uint8,
     ``qift_paged_attention_workspace`` bytes) is allocated on the call's stream if not given.  Rows of a new result
     that belong to no sequence are not initialised."""
-    pages, kv_heads, size, d = _cache(k_cache, k_scales, v_cache, v_scales)
-    qs = _head_rows(q, "q")
-    T, hq, _ = q.shape
-    _shape(q, "q", (T, hq, d))
+    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [tokens, q_heads, head_dim] tensor")
+    shape = q.shape
+    T, hq = shape[0], shape[1]
+    q_at, q_row = _heads(q, "q", (T, hq, d), index)
     _2d(_cuda(page_table, "page_table", torch.int32), "page_table")
     B, max_pages = page_table.shape
-    _shape(_cuda(kv_lens, "kv_lens", torch.int32), "kv_lens", (B,))
+    table_at = _is(page_table, "page_table", torch.int32, (B, max_pages), index)
+    lens_at = _is(kv_lens, "kv_lens", torch.int32, (B,), index)
+    cu_at = prefix_at = lse_at = None
     if cu_q is not None:
-        _shape(_cuda(cu_q, "cu_q", torch.int32), "cu_q", (B + 1,))
+        cu_at = _is(cu_q, "cu_q", torch.int32, (B + 1,), index)
     elif T != B * max_q:
         raise ValueError(f"without cu_q, q must have batch * max_q = {B * max_q} rows, got {T}")
     if prefix_table is not None:
         _at_least(_cuda(prefix_table, "prefix_table", torch.int32), "prefix_table", -(-prefix_len // size))
+        prefix_at = _is(prefix_table, "prefix_table", torch.int32, prefix_table.shape, index)
     elif prefix_len != 0:
         raise ValueError("prefix_len needs prefix_table")
-    if out_dtype not in (torch.float16, torch.float32):
+    if out_dtype is not torch.float16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be torch.float16 or torch.float32")
-    if out is not None:
-        _shape(_cuda(out, "out", out_dtype), "out", (T, hq, d))
     if lse is not None:
-        _shape(_cuda(lse, "lse", torch.float32), "lse", (T, hq))
-    dev = _same_device(("q", q), ("cu_q", cu_q), ("k_cache", k_cache), ("k_scales", k_scales), ("v_cache", v_cache),
-                       ("v_scales", v_scales), ("page_table", page_table), ("kv_lens", kv_lens),
-                       ("prefix_table", prefix_table), ("out", out), ("lse", lse), ("workspace", workspace))
-    L = lib()
-    need = L.qift_paged_attention_workspace(T, hq, kv_heads, d, B, max_q, size, max_pages, max_kv, prefix_len, window,
-                                            sinks)
+        lse_at = _is(lse, "lse", torch.float32, (T, hq), index)
+    need = _workspace_bytes(T, hq, kv_heads, d, B, max_q, size, max_pages, max_kv, prefix_len, window, sinks)
+    ws_at, ws_bytes = None, 0
     if workspace is not None:
-        _at_least(_cuda(workspace, "workspace", torch.uint8), "workspace", max(need, 0))
+        _at_least(_cuda(workspace, "workspace", torch.uint8), "workspace", need)
+        ws_at, ws_bytes = _is(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
     elif need > 0:
-        if stream is None or stream == torch.cuda.current_stream(dev):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:  # freed, and used again, in the order of the stream that runs the kernels
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    y = torch.empty((T, hq, d), dtype=out_dtype, device=dev) if out is None else out
-    with _on(dev):
-        _check(L.qift_paged_attention(_ptr(q), qs, T, hq, kv_heads, d, _ptr(cu_q), B, max_q, _ptr(k_cache),
-                                      _ptr(k_scales), _ptr(v_cache), _ptr(v_scales), pages, size, _ptr(page_table),
-                                      max_pages, _ptr(kv_lens), max_kv, _ptr(prefix_table), prefix_len, window, sinks,
-                                      1.0 / math.sqrt(d) if scale is None else scale, block, _ptr(y),
-                                      QIFT_F16 if out_dtype == torch.float16 else QIFT_F32, _ptr(lse), _ptr(workspace),
-                                      workspace.numel() if workspace is not None else 0, _stream(stream, dev)),
-               "qift_paged_attention")
-    return y
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_at, ws_bytes = workspace.data_ptr(), need
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        out_at = out.data_ptr()
+    else:
+        out_at = _is(out, "out", out_dtype, shape, index)
+    _check(_launch(index, stream, lib().qift_paged_attention, q_at, q_row, T, hq, kv_heads, d, cu_at, B, max_q, kc, ks,
+                   vc, vs, pages, size, table_at, max_pages, lens_at, max_kv, prefix_at, prefix_len, window, sinks,
+                   1.0 / math.sqrt(d) if scale is None else scale, block, out_at,
+                   QIFT_F16 if out_dtype is torch.float16 else QIFT_F32, lse_at, ws_at, ws_bytes),
+           "qift_paged_attention")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(*sizes: int) -> int:
+    return lib().qift_paged_attention_workspace(*sizes)
 
 
 def qift_paged_attention_workspace(tokens: int, q_heads: int, kv_heads: int, head_dim: int, batch: int, max_q: int,
                                    page_size: int, max_pages: int, max_kv: int = 0, prefix_len: int = 0,
                                    window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace that ``qift_paged_attention`` needs for these sizes; raises if it would refuse them."""
-    n = lib().qift_paged_attention_workspace(tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages,
-                                             max_kv, prefix_len, window, sinks)
+    n = _workspace_bytes(tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv, prefix_len,
+                         window, sinks)
     if n < 0:
         raise ValueError("qift_paged_attention would refuse these sizes")
     return n

@@ -21,6 +21,7 @@
 // of u_j + log2 t_j, so the rounded weights lie in [0, 2^15] whatever the size of the values, and
 // keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -31,13 +32,15 @@ namespace attn {
 
 constexpr int kWarps = 4;
 constexpr int kStep = 32;  // keys a warp takes at a time
-constexpr float kSlack = 7.0f, kLift = 8.0f;  // weights are at most 2^(kSlack + kLift) = 2^15 < 65504
+// A row's reference `refl` is kLift below the largest u_j + log2 t_j when it was last raised; weights may grow
+// to kMostWeight < 65504 before it is raised again.
+constexpr float kLift = 8.0f, kMostWeight = 32768.0f;
 
 template <int D>
 struct Shape {
     static constexpr int ROW = D / 2;                      // bytes of a key's codes
     static constexpr int STAGE = 2 * kStep * ROW + 2 * kStep * 4;
-    static constexpr int STAGES = D == 256 ? 3 : 4;
+    static constexpr int STAGES = 3;
     static constexpr int KW = D / 32, VW = D / 64;         // 32-bit words of a key, of a value, a lane holds
     static constexpr int MT = D / 16;                      // 16-high tiles of O^T
     static constexpr int OPAD = D + 4;
@@ -64,9 +67,25 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
 }
 // Two two's-complement nibbles, 16 bits apart, as binary16: from bits 0-3 exactly, from bits 4-7
 // plus 72 (1 x 2^6 with the nibble, its sign bit flipped, above the last four bits), or exactly.
-__device__ __forceinline__ uint32_t nib_lo(uint32_t w) { return sub2((w & 0x000F000Fu) ^ 0x64086408u, 0x64086408u); }
-__device__ __forceinline__ uint32_t nib_hi72(uint32_t w) { return (w & 0x00F000F0u) ^ 0x54805480u; }
-__device__ __forceinline__ uint32_t nib_hi(uint32_t w) { return sub2(nib_hi72(w), 0x54805480u); }
+// Mask and flip are one three-input operation each; it takes one immediate at most, so the constants
+// are kept in registers (given as immediates, the compiler makes two operations of it).
+struct Nibbles {
+    uint32_t mask_lo, mask_hi, one_lo, one_hi;
+    __device__ __forceinline__ Nibbles() {
+        asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask_lo));
+        asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask_hi));
+        asm volatile("mov.b32 %0, 0x64086408;" : "=r"(one_lo));
+        asm volatile("mov.b32 %0, 0x54805480;" : "=r"(one_hi));
+    }
+    __device__ __forceinline__ static uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) {
+        uint32_t r;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(m), "r"(c));  // (w & m) ^ c
+        return r;
+    }
+    __device__ __forceinline__ uint32_t lo(uint32_t w) const { return sub2(and_xor(w, mask_lo, one_lo), one_lo); }
+    __device__ __forceinline__ uint32_t hi72(uint32_t w) const { return and_xor(w, mask_hi, one_hi); }
+    __device__ __forceinline__ uint32_t hi(uint32_t w) const { return sub2(hi72(w), one_hi); }
+};
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -109,7 +128,7 @@ template <int D, int NR>
 __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs a, const Deal deal) {
     using S = Shape<D>;
     constexpr int R = 8 * NR;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];  // rows of codes are swizzled by address bits 5 and 6
     __shared__ int64_t row_token[R];
     __shared__ int row_pos[R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -162,6 +181,8 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
     if (pmax >= 0) range = visible<kStep>(a, pmin, pmax, base, capacity);
     // The host's chunk covers lengths up to its bound; a longer sequence takes longer splits.
     const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
+    // A step of which every row sees all: up to `sure`, and above `sure_low` or among the sinks.
+    const int sure = min(pmin, base + range.limit - 1), sure_low = a.window ? pmax - a.window : -1;
     const int s_begin = min(split * chunk, range.steps), s_end = min(s_begin + chunk, range.steps);
 
     // ---- this lane's rows: column g of a tile as a right operand, columns 2t and 2t + 1 as a result
@@ -195,54 +216,60 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
         }
     }
 
+    const Nibbles nib;
     float o[NR][S::MT][4];
-    float ref[NR][2], sum[NR][2];
+    float refl[NR][2], sum[NR][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
 #pragma unroll
         for (int m = 0; m < S::MT; ++m)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[n][m][c] = 0.0f;
-        ref[n][0] = ref[n][1] = kNone;
+        refl[n][0] = refl[n][1] = kNone;
         sum[n][0] = sum[n][1] = 0.0f;
     }
 
-    // ---- the ring of this warp: lanes 0-15 copy the first 16 keys of a step, lanes 16-31 the rest
+    // ---- the ring of this warp: lanes 0-15 copy the first 16 keys of a step, lanes 16-31 the rest.
+    // A lane's piece i (16 bytes) is piece c of key tok = l16 / CH + i * (16 / CH).  Keys lie in the order of
+    // the product's rows (row r is key (r & 8) + (r & 1) * 4 + (r & 7) / 2), and pieces are swapped so that the
+    // lanes' reads meet no bank twice; both are linear over the bits of the index, so a lane keeps the part
+    // of its own bits and the part of i is a constant.
     uint8_t* ring = smem + warp * (S::STAGES * S::STAGE);
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int half = lane >> 4, l16 = lane & 15;
+    constexpr int CH = S::ROW / 16;
+    auto row_of = [](int tok) { return (tok & 8) | ((tok & 3) << 1) | ((tok >> 2) & 1); };
+    auto k_swap = [](int r) { return D == 256 ? (r & 1) * 64 : 0; };
+    auto v_swap = [](int tok) { return D == 256 ? (tok & 3) * 32 : D == 128 ? ((tok >> 1) & 1) * 32 : 0; };
+    const int tok0 = l16 / CH, c0 = l16 % CH;
+    const uint32_t k_dst = ring32 + (half * 16 + row_of(tok0)) * S::ROW + ((c0 * 16) ^ k_swap(row_of(tok0)));
+    const uint32_t v_dst = ring32 + (kStep + half * 16 + tok0) * S::ROW + ((c0 * 16) ^ v_swap(tok0));
+    const uint32_t s_dst = ring32 + 2 * kStep * S::ROW + lane * 4;
     const int page_mask = (1 << a.log_page) - 1;
+    const int shift = range.main - range.head;
     // Page of this lane's half of a step, -1 where there is none.
     auto page_of = [&](int s) -> int {
-        if (s >= s_end) return -1;
-        const int j = range.block(s) * kStep + half * 16;
-        if (j >= range.limit) return -1;
+        const int j = (s + (s >= range.head ? shift : 0)) * kStep + half * 16;
+        if (s >= s_end || j >= range.limit) return -1;
         const int p = table[j >> a.log_page];
         return (uint32_t)p < (uint64_t)a.n_pages ? p : -1;
     };
     auto issue = [&](int s, int stage, int page) {
         if (page >= 0) {
-            const int off = (range.block(s) * kStep + half * 16) & page_mask;
+            const int off = ((s + (s >= range.head ? shift : 0)) * kStep + half * 16) & page_mask;
             const int64_t at = (((int64_t)page * a.kv_heads + h) << a.log_page) + off;
             if (QIFT_CK_RANGE(at, 16, (a.n_pages * a.kv_heads) << a.log_page)) {
-                const uint8_t* ks = a.k_cache + at * S::ROW;
-                const uint8_t* vs = a.v_cache + at * S::ROW;
-                const uint32_t dst = ring32 + stage * S::STAGE + half * 16 * S::ROW;
-                constexpr int CH = S::ROW / 16;  // 16-byte pieces of a row
+                const uint8_t* ks = a.k_cache + at * S::ROW + l16 * 16;
+                const uint8_t* vs = a.v_cache + at * S::ROW + l16 * 16;
+                const uint32_t to = stage * S::STAGE;
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
-                    const int tok = (l16 + 16 * i) / CH, c = (l16 + 16 * i) % CH;
-                    // Keys lie in the order of the product's rows (row r is key (r & 8) + (r & 1) * 4 +
-                    // (r & 7) / 2); pieces are swapped so that the lanes' reads meet no bank twice.
-                    const int r = (tok & 8) | ((tok & 3) << 1) | ((tok >> 2) & 1);
-                    const int kc = D == 256 ? c ^ ((r & 1) * 4) : c;
-                    const int vc = D == 256 ? c ^ ((tok & 3) * 2) : D == 128 ? c ^ (((tok >> 1) & 1) * 2) : c;
-                    cp16(dst + r * S::ROW + kc * 16, ks + (l16 + 16 * i) * 16);
-                    cp16(dst + kStep * S::ROW + tok * S::ROW + vc * 16, vs + (l16 + 16 * i) * 16);
+                    const int tok = i * (16 / CH), r = row_of(tok);
+                    cp16((k_dst + to + r * S::ROW) ^ k_swap(r), ks + i * 256);
+                    cp16((v_dst + to + tok * S::ROW) ^ v_swap(tok), vs + i * 256);
                 }
-                const uint32_t sc = ring32 + stage * S::STAGE + 2 * kStep * S::ROW + lane * 4;
-                cp4(sc, a.k_scales + at + l16);
-                cp4(sc + kStep * 4, a.v_scales + at + l16);
+                cp4(s_dst + to, a.k_scales + at + l16);
+                cp4(s_dst + to + kStep * 4, a.v_scales + at + l16);
             }
         }
         cp_commit();
@@ -274,22 +301,19 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
         __syncwarp();
         const uint8_t* st = ring + stage * S::STAGE;
         const float* scales = reinterpret_cast<const float*>(st + 2 * kStep * S::ROW);
-        const int j0 = base + range.block(s) * kStep;  // position of the step's first key
+        const int j0 = base + (s + (s >= range.head ? shift : 0)) * kStep;  // position of the step's first key
         const uint32_t has = (there >> (2 * stage)) & 3u;
-        const bool all = has == 3u && j0 + kStep - 1 <= pmin && (!a.window || j0 > pmax - a.window || j0 + kStep <= a.sinks) &&
-                         j0 - base + kStep <= range.limit;
+        const bool all = has == 3u && j0 + kStep - 1 <= sure && (j0 > sure_low || j0 + kStep <= a.sinks);
 
-        // ---- scores, in log2 units
-        float x[2][NR][4], vs[2][2], lv[2][2];
+        // ---- scores
+        float x[2][NR][4], ks[2][2], vs[2][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int row = c * 16 + (g & 1) * 4 + (g >> 1);  // key of product row g; row g + 8 is 8 further
-            float ks[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ks[e] = scales[row + 8 * e] * a.scale_log2;
+                ks[c][e] = scales[row + 8 * e] * a.scale_log2;
                 vs[c][e] = scales[kStep + row + 8 * e];
-                lv[c][e] = fmaxf(lg2(vs[c][e]), -28.0f);  // the smallest scale is 2^-24 / 7
             }
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -309,22 +333,22 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                     uint32_t a0 = w0[w], a1 = w1[w];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t l0 = nib_lo(a0), l1 = nib_lo(a1), h0 = nib_hi72(a0), h1 = nib_hi72(a1);
+                        const uint32_t l0 = nib.lo(a0), l1 = nib.lo(a1), h0 = nib.hi72(a0), h1 = nib.hi72(a1);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) mma16816(x[c][n], l0, l1, h0, h1, qf[n][k][2 * e], qf[n][k][2 * e + 1]);
                         a0 >>= 8, a1 >>= 8;
                     }
                 }
             }
+        }
+        // Masked scores become -infinity (their scale, which may hold anything, is multiplied in first), and
+        // what no row sees gets the value scale 0.
+        if (!all) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                x[c][n][0] *= ks[0], x[c][n][1] *= ks[0];
-                x[c][n][2] *= ks[1], x[c][n][3] *= ks[1];
-            }
-            if (!all) {
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = j0 + row + 8 * e;
+                    const int j = j0 + c * 16 + (g & 1) * 4 + (g >> 1) + 8 * e;
                     const bool in = ((has >> c) & 1u) && j - base < range.limit;
                     bool any = false;
 #pragma unroll
@@ -333,40 +357,55 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                         for (int q = 0; q < 2; ++q) {
                             const int p = pos[n][q];
                             const bool see = in && j <= p && (!a.window || j > p - a.window || j < a.sinks);
-                            if (!see) x[c][n][2 * e + q] = -INFINITY;
+                            x[c][n][2 * e + q] = see ? x[c][n][2 * e + q] * ks[c][e] : -INFINITY;
                             any |= see;
                         }
-                    // What no row sees may hold anything: its scale must not reach the sums.
-                    if (!any) vs[c][e] = 0.0f, lv[c][e] = -28.0f;
+                    ks[c][e] = 1.0f;
+                    if (!any) vs[c][e] = 0.0f;
                 }
-            }
         }
 
-        // ---- the reference: raised, and what is summed so far scaled down, only where a weight would
-        // pass 2^(kSlack + kLift); the same for every lane of a row, so a vote decides
+        // ---- weights, by the reference so far.  It is raised, and what is summed scaled down, only where a
+        // weight would pass kMostWeight (or is no number: an overflow times a scale of 0); a vote
+        // decides, so all lanes of a row agree.
+        float wt[2][NR][4], wv[2][NR][4];
+        auto weigh = [&]() {
+            bool fits = true;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            float top[2];
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                top[q] = fmaxf(fmaxf(x[0][n][q] + lv[0][0], x[0][n][2 + q] + lv[0][1]),
-                               fmaxf(x[1][n][q] + lv[1][0], x[1][n][2 + q] + lv[1][1]));
-            if (__any_sync(0xffffffffu, top[0] > ref[n][0] + kSlack || top[1] > ref[n][1] + kSlack)) {
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wt[c][n][i] = ex2(__fmaf_rn(x[c][n][i], ks[c][i >> 1], -refl[n][i & 1]));
+                        wv[c][n][i] = wt[c][n][i] * vs[c][i >> 1];
+                        fits = fits && wv[c][n][i] <= kMostWeight;
+                    }
+            return fits;
+        };
+        if (!__all_sync(0xffffffffu, weigh())) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
+                    float top = refl[n][q] + kLift;
 #pragma unroll
-                    for (int m = 4; m < 32; m <<= 1) top[q] = fmaxf(top[q], __shfl_xor_sync(0xffffffffu, top[q], m));
-                    const float to = fmaxf(ref[n][q], top[q]);
-                    const float down = ex2(ref[n][q] - to);
-                    ref[n][q] = to;
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)  // the smallest scale is 2^-24 / 7
+                            top = fmaxf(top, __fmaf_rn(x[c][n][2 * e + q], ks[c][e], fmaxf(lg2(vs[c][e]), -28.0f)));
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+                    const float down = ex2(refl[n][q] + kLift - top);
+                    refl[n][q] = top - kLift;
                     sum[n][q] *= down;
 #pragma unroll
                     for (int m = 0; m < S::MT; ++m) o[n][m][q] *= down, o[n][m][2 + q] *= down;
                 }
-            }
+            weigh();
         }
 
-        // ---- weights and the second product
+        // ---- the second product
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             uint32_t p[NR][2];
@@ -374,11 +413,9 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
             for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float w0 = ex2(x[c][n][2 * e] - (ref[n][0] - kLift));
-                    const float w1 = ex2(x[c][n][2 * e + 1] - (ref[n][1] - kLift));
-                    sum[n][0] += w0;
-                    sum[n][1] += w1;
-                    const __half2 h2 = __floats2half2_rn(w0 * vs[c][e], w1 * vs[c][e]);
+                    sum[n][0] += wt[c][n][2 * e];
+                    sum[n][1] += wt[c][n][2 * e + 1];
+                    const __half2 h2 = __floats2half2_rn(wv[c][n][2 * e], wv[c][n][2 * e + 1]);
                     p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h2));
                 }
             constexpr int VB = S::VW * 4;
@@ -386,9 +423,7 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = t + 4 * i;  // product indexes 2t, 2t + 1, 2t + 8, 2t + 9
-                const int at = D == 256   ? (g ^ ((tok & 3) * 2)) * 16
-                               : D == 128 ? ((g >> 1) ^ (((tok >> 1) & 1) * 2)) * 16 + (g & 1) * 8
-                                          : g * 4;
+                const int at = (D == 256 ? g * 16 : D == 128 ? g * 8 : g * 4) ^ v_swap(tok);
                 lds<VB>(v[i], st + kStep * S::ROW + (c * 16 + tok) * S::ROW + at);
             }
 #pragma unroll
@@ -399,7 +434,7 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                     uint32_t hi = prmt(v[2][w], v[3][w], u ? 0x7632u : 0x5410u);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t a0 = nib_lo(lo), a1 = nib_hi(lo), a2 = nib_lo(hi), a3 = nib_hi(hi);
+                        const uint32_t a0 = nib.lo(lo), a1 = nib.hi(lo), a2 = nib.lo(hi), a3 = nib.hi(hi);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) mma16816(o[n][w * 4 + u * 2 + e], a0, a1, a2, a3, p[n][0], p[n][1]);
                         lo >>= 8, hi >>= 8;
@@ -428,7 +463,7 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                 *reinterpret_cast<float4*>(dst + 2 * m) =
                     make_float4(o[n][m][q], o[n][m][2 + q], o[n][m + 1][q], o[n][m + 1][2 + q]);
             if (g == 0) {
-                pm[(warp * R + r) * 2] = ref[n][q];
+                pm[(warp * R + r) * 2] = refl[n][q];
                 pm[(warp * R + r) * 2 + 1] = sum[n][q];
             }
         }
@@ -452,7 +487,6 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] += f * src[i];
         }
-        M -= kLift;
         if (deal.slots == 0) {
             finish_row<D>(a, acc, M, L, token, head, lane);
         } else {
@@ -467,19 +501,22 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
     }
 }
 
-// Joins the partial results of a row: one warp a row, rows dealt out as (sequence, token, head).
+// Joins the partial results of a row: one block of kJoinWarps warps a row, each warp every
+// kJoinWarps-th slot, the slots' (M, L) read by all lanes at once; rows are dealt out as (sequence,
+// token, head).
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const AttentionArgs a, const int slots) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionArgs a, const int slots) {
     constexpr int E = D / 32;
+    __shared__ float part[kJoinWarps][D], part_l[kJoinWarps];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t row = blockIdx.x;
     const int head = (int)(row % a.q_heads);
     row /= a.q_heads;
     const int i = (int)(row % a.max_q);
     const int64_t b = row / a.max_q;
-    if (b >= a.batch) return;
     const Sequence s = sequence(a, (int)b);
     if (i >= s.q_len) return;
     const int64_t token = s.first + i;
@@ -492,14 +529,36 @@ __global__ void __launch_bounds__(256) join_kernel(const AttentionArgs a, const 
     float L = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int k = 0; k < slots; ++k) {
-        const float2 ml = p.ml[at + k];
-        if (!(ml.y > 0.0f)) continue;
-        const float f = ex2(ml.x - M);
+    for (int k0 = 0; k0 < slots; k0 += 32 * kJoinWarps) {
+        const int mine = k0 + warp + lane * kJoinWarps;
+        const float2 ml = mine < slots ? p.ml[at + mine] : make_float2(kNone, 0.0f);
+        const float f = ml.y > 0.0f ? ex2(ml.x - M) : 0.0f;
         L += f * ml.y;
-        const float* src = p.o + (at + k) * D + lane * E;
+        uint32_t full = __ballot_sync(0xffffffffu, ml.y > 0.0f);
+        while (full) {
+            const int l = __ffs(full) - 1;
+            full &= full - 1;
+            const float w = __shfl_sync(0xffffffffu, f, l);
+            const float* src = p.o + (at + k0 + warp + l * kJoinWarps) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * src[e];
+            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(w, src[e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+    if (lane == 0) part_l[warp] = L;
+    __syncthreads();
+    if (warp != 0) return;
+    L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        L += part_l[w];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += part[w][lane * E + e];
     }
     finish_row<D>(a, acc, M, L, token, head, lane);
 }
@@ -509,7 +568,7 @@ static Deal deal_out(const AttentionArgs& a, int rows) {
     Deal d = {};
     d.own_tiles = (int)(((int64_t)a.max_q * G + rows - 1) / rows);
     // Blocks enough for four turns of every SM's room, but no split under 512 keys (four steps a warp).
-    const int64_t want = 148 * 3 * 4, least = 16;
+    const int64_t want = getenv("QW") ? atoi(getenv("QW")) : 148 * 3 * 4, least = getenv("QL") ? atoi(getenv("QL")) : 16;
     auto split = [&](int64_t blocks, int64_t keys, int* splits, int* chunk) {
         const int64_t steps = (keys + kStep - 1) / kStep + 1;
         int64_t n = (want + blocks - 1) / blocks;
@@ -551,8 +610,8 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, stream_kernel<D, NR>, a, d);
     if (e != cudaSuccess || d.slots == 0) return e;
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.batch * a.max_q * a.q_heads + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.max_q * a.q_heads));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, d.slots);
 }
@@ -574,7 +633,7 @@ static cudaError_t launch_rows_of(const AttentionArgs& a, cudaStream_t s) {
 
 bool attention_supported(const AttentionArgs& a) {
     const attn::Deal d = attn::deal_out(a, attn::rows_per_block(a));
-    return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads / 8 < 0x7fffffff;
+    return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads <= 0x7fffffff;
 }
 
 int64_t attention_workspace_bytes(const AttentionArgs& a) {
