@@ -329,6 +329,13 @@ def test_sequences_that_end_inside_the_prefix():
     check(m, 20, 3)
 
 
+def test_an_empty_sequence_among_long_ones_sees_nothing():
+    # the prefix's rows are those of the whole batch: one that sees nothing lies between rows that see all
+    m = make([1] * 9 + [3], [400 + b for b in range(4)] + [0] + [500 + b for b in range(4)] + [2], 4, 2, 128, 16,
+             prefix=300, seed=19)
+    check(m)
+
+
 def test_prefix_for_many_rows_equals_its_keys_in_every_table():
     # The same keys, once as a prefix and once as pages that all tables begin with: the same sums in another order.
     hq, hk, d, size, prefix = 32, 8, 128, 16, 640

@@ -31,7 +31,7 @@ def _append(L, **kw):
     dict(q=None), dict(q_out=None), dict(q_heads=0), dict(k=None), dict(v=None), dict(slots=None),
     dict(positions=None), dict(kc=None), dict(vs=None),
     dict(q_stride=6140), dict(q_stride=4088), dict(k_stride=1016), dict(v_stride=0), dict(k_stride=2 ** 62),
-    dict(k=A + 8), dict(q_out=(A << 10) + 2), dict(kc=A + 8), dict(rope=A + 4), dict(slots=A + 4), dict(ks=A + 2),
+    dict(k=A + 8), dict(q_out=(A << 10) + 2), dict(kc=A + 8), dict(rope=A + 4), dict(slots=A + 4), dict(ks=A + 4),
     dict(block=3), dict(block=256), dict(block=-2), dict(rope_dim=144), dict(rope_dim=0), dict(rope_dim=17),
     dict(inter=2), dict(rope_len=-1),
     dict(q_out=A), dict(q_out=A + 45056 - 16), dict(q_out=(A << 8) - 16), dict(q_out=A << 9),  # overlaps
@@ -81,7 +81,7 @@ def _attention(L, **kw):
     dict(tokens=-1), dict(batch=-1), dict(max_q=-1), dict(q_heads=0), dict(q_heads=33), dict(kv_heads=0),
     dict(max_pages=-1), dict(max_kv=-1), dict(prefix_len=-1), dict(window=-1), dict(sinks=-1), dict(dt=2),
     dict(q=None), dict(out=None), dict(kv_lens=None), dict(table=None), dict(prefix_len=5), dict(kc=None), dict(ks=None),
-    dict(cu_q=None), dict(q=A + 8), dict(out=A + 8), dict(kc=A + 4), dict(vs=A + 2), dict(table=A + 1), dict(lse=A + 2),
+    dict(cu_q=None), dict(q=A + 8), dict(out=A + 8), dict(kc=A + 4), dict(vs=A + 4), dict(table=A + 1), dict(lse=A + 2),
     dict(q_stride=4092), dict(q_stride=4088), dict(block=6), dict(block=256), dict(scale=float("nan")),
     dict(scale=float("inf")),
     dict(prefix=A, prefix_len=50, ws=None), dict(prefix=A, prefix_len=50, ws_bytes=16),

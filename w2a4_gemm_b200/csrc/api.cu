@@ -35,7 +35,7 @@ qift_status cache_shape(int64_t n_pages, int32_t page_size, int32_t kv_heads, in
     if (n_pages < 0 || page_size <= 0 || kv_heads <= 0 || head_dim <= 0) return QIFT_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QIFT_ERR_UNSUPPORTED;
     if (!is_pow2(page_size) || page_size < 16 || page_size > 4096) return QIFT_ERR_UNSUPPORTED;
-    if (kv_heads > 1 << 16 || n_pages > INT64_MAX / kv_heads / page_size / head_dim) return QIFT_ERR_UNSUPPORTED;
+    if (kv_heads > 1 << 16 || n_pages > 0xfffffff0LL * 16 / kv_heads / page_size) return QIFT_ERR_UNSUPPORTED;  // a place is 16 rows, in 32 bits
     return QIFT_OK;
 }
 int log2_of(int32_t v) {
@@ -324,7 +324,7 @@ qift_status qift_append_kv(const void* q, int64_t q_stride, const void* k, int64
     if (!k || !v || !slots || (rope && !positions)) return QIFT_ERR_INVALID_ARG;
     if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
-        !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) || !aligned4(v_scales) ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales) ||
         !aligned8(slots) || !aligned8(positions))
         return QIFT_ERR_INVALID_ARG;
     const int64_t q_row = (int64_t)q_heads * head_dim, kv_row = (int64_t)kv_heads * head_dim;
@@ -378,7 +378,7 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
     if (tokens == 0) return QIFT_OK;
     if (!slots || !k_out || !v_out) return QIFT_ERR_INVALID_ARG;
     if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
-    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) || !aligned4(v_scales) || !aligned8(slots) ||
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) || !aligned16(v_scales) || !aligned8(slots) ||
         !aligned16(k_out) || !aligned16(v_out))
         return QIFT_ERR_INVALID_ARG;
     qift::GatherArgs a = {};
@@ -428,8 +428,8 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
     if (!q || !out || !kv_lens || (max_pages > 0 && !page_table) || (prefix_len > 0 && !prefix_table))
         return QIFT_ERR_INVALID_ARG;
     if (n_pages > 0 && (!k_cache || !k_scales || !v_cache || !v_scales)) return QIFT_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(k_scales) ||
-        !aligned4(v_scales) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(page_table) ||
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
+        !aligned16(v_scales) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(page_table) ||
         !aligned4(prefix_table) || !aligned4(lse) || !aligned16(workspace))
         return QIFT_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride < (int64_t)q_heads * head_dim || q_stride > INT64_MAX / 4 / tokens)

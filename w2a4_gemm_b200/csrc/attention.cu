@@ -21,7 +21,6 @@
 // of u_j + log2 t_j, so the rounded weights lie in [0, 2^15] whatever the size of the values, and
 // keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -40,7 +39,7 @@ template <int D>
 struct Shape {
     static constexpr int ROW = D / 2;                      // bytes of a key's codes
     static constexpr int STAGE = 2 * kStep * ROW + 2 * kStep * 4;
-    static constexpr int STAGES = 3;
+    static constexpr int STAGES = 2;
     static constexpr int KW = D / 32, VW = D / 64;         // 32-bit words of a key, of a value, a lane holds
     static constexpr int MT = D / 16;                      // 16-high tiles of O^T
     static constexpr int OPAD = D + 4;
@@ -93,6 +92,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with the accumulator's start values (columns 2t, 2t + 1) in registers of their own.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], float s0, float s1, uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(s0), "f"(s1));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -125,7 +131,7 @@ struct Deal {
 
 // Eight query rows are the columns of one product tile; NR of them a block.
 template <int D, int NR>
-__global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs a, const Deal deal) {
+__global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stream_kernel(const AttentionArgs a, const Deal deal) {
     using S = Shape<D>;
     constexpr int R = 8 * NR;
     extern __shared__ __align__(128) uint8_t smem[];  // rows of codes are swizzled by address bits 5 and 6
@@ -171,18 +177,26 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
         row_pos[threadIdx.x] = pos;
     }
     __syncthreads();
-    int pmin = 0x7fffffff, pmax = -1;
+    int pmin = 0x7fffffff, pmax = -1, least = 0x7fffffff;  // least: rows that see nothing (-1) included
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int p = row_pos[r];
+        if (row_token[r] >= 0) least = min(least, p);
         if (p >= 0) pmin = min(pmin, p), pmax = max(pmax, p);
     }
     Range range = {0, 0, 0, 0};
     if (pmax >= 0) range = visible<kStep>(a, pmin, pmax, base, capacity);
     // The host's chunk covers lengths up to its bound; a longer sequence takes longer splits.
     const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
-    // A step of which every row sees all: up to `sure`, and above `sure_low` or among the sinks.
-    const int sure = min(pmin, base + range.limit - 1), sure_low = a.window ? pmax - a.window : -1;
+    // The steps, from sure_from on, of which every row sees every key: inside all rows' windows.
+    int sure_from = range.head;
+    uint32_t sure_steps = 0;
+    {
+        const int end = min(least + 1 - base, range.limit) / kStep;  // blocks wholly before the first row's position
+        const int from = a.window ? (max(pmax - a.window + 1 - base, 0) + kStep - 1) / kStep : 0;
+        const int first = max(from, range.main);
+        if (pmax >= 0 && end > first) sure_from = first - (range.main - range.head), sure_steps = end - first;
+    }
     const int s_begin = min(split * chunk, range.steps), s_end = min(s_begin + chunk, range.steps);
 
     // ---- this lane's rows: column g of a tile as a right operand, columns 2t and 2t + 1 as a result
@@ -244,82 +258,72 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
     const int tok0 = l16 / CH, c0 = l16 % CH;
     const uint32_t k_dst = ring32 + (half * 16 + row_of(tok0)) * S::ROW + ((c0 * 16) ^ k_swap(row_of(tok0)));
     const uint32_t v_dst = ring32 + (kStep + half * 16 + tok0) * S::ROW + ((c0 * 16) ^ v_swap(tok0));
-    const uint32_t s_dst = ring32 + 2 * kStep * S::ROW + lane * 4;
-    const int page_mask = (1 << a.log_page) - 1;
+    // A lane reads the scales of keys k8, k8 + 8, + 16, + 24 at once: they lie side by side.
+    const uint32_t s_dst = ring32 + 2 * kStep * S::ROW + ((l16 & 7) * 4 + half * 2 + (l16 >> 3)) * 4;
     const int shift = range.main - range.head;
-    // Page of this lane's half of a step, -1 where there is none.
-    auto page_of = [&](int s) -> int {
-        const int j = (s + (s >= range.head ? shift : 0)) * kStep + half * 16;
-        if (s >= s_end || j >= range.limit) return -1;
-        const int p = table[j >> a.log_page];
-        return (uint32_t)p < (uint64_t)a.n_pages ? p : -1;
+    const int page_mask = (1 << a.log_page) - 1;
+    // Where 16 keys lie in the pool, counted in 16s, for 16 turns of this warp at once: lane 2 i + half
+    // holds turn i's.  kNowhere: the page is not there, or the sequence ends before.
+    constexpr uint32_t kNowhere = 0xffffffffu;
+    uint32_t places = kNowhere;
+    bool lost = false;  // a page that should be there was not: every step is looked at key by key
+    auto find = [&](int turn) {
+        const int s = s_begin + warp + (turn + (lane >> 1)) * kWarps;
+        const int j = (s + (s >= range.head ? shift : 0)) * kStep + (lane & 1) * 16;
+        places = kNowhere;
+        if (s < s_end && j < range.limit) {
+            const int page = table[j >> a.log_page];
+            if ((uint32_t)page < (uint64_t)a.n_pages)
+                places = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & page_mask)) >> 4);
+            else
+                lost = true;
+        }
+        lost = __any_sync(0xffffffffu, lost);
     };
-    auto issue = [&](int s, int stage, int page) {
-        if (page >= 0) {
-            const int off = ((s + (s >= range.head ? shift : 0)) * kStep + half * 16) & page_mask;
-            const int64_t at = (((int64_t)page * a.kv_heads + h) << a.log_page) + off;
-            if (QIFT_CK_RANGE(at, 16, (a.n_pages * a.kv_heads) << a.log_page)) {
-                const uint8_t* ks = a.k_cache + at * S::ROW + l16 * 16;
-                const uint8_t* vs = a.v_cache + at * S::ROW + l16 * 16;
-                const uint32_t to = stage * S::STAGE;
+    const uint8_t* k_src = a.k_cache + l16 * 16;
+    const uint8_t* v_src = a.v_cache + l16 * 16;
+    const float* ks_src = a.k_scales + l16;
+    const float* vs_src = a.v_scales + l16;
+    auto issue = [&](int turn, int stage) {
+        if ((turn & 15) == 0) find(turn);
+        const uint32_t at = __shfl_sync(0xffffffffu, places, 2 * (turn & 15) + half);
+        const uint32_t to = stage * S::STAGE;
+        if (at != kNowhere && QIFT_CK((int64_t)at * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page)) {
+            const uint8_t* ks = k_src + (uint64_t)at * (16 * S::ROW);
+            const uint8_t* vs = v_src + (uint64_t)at * (16 * S::ROW);
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int tok = i * (16 / CH), r = row_of(tok);
-                    cp16((k_dst + to + r * S::ROW) ^ k_swap(r), ks + i * 256);
-                    cp16((v_dst + to + tok * S::ROW) ^ v_swap(tok), vs + i * 256);
-                }
-                cp4(s_dst + to, a.k_scales + at + l16);
-                cp4(s_dst + to + kStep * 4, a.v_scales + at + l16);
+            for (int i = 0; i < CH; ++i) {
+                const int tok = i * (16 / CH), r = row_of(tok);
+                cp16((k_dst + to + r * S::ROW) ^ k_swap(r), ks + i * 256);
+                cp16((v_dst + to + tok * S::ROW) ^ v_swap(tok), vs + i * 256);
             }
+            cp4(s_dst + to, ks_src + (uint64_t)at * 16);
+            cp4(s_dst + to + kStep * 4, vs_src + (uint64_t)at * 16);
+        } else {  // a scale below 0 marks keys that are not there
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_dst + to), "f"(-1.0f) : "memory");
         }
         cp_commit();
     };
 
-    int page_next = page_of(s_begin + warp);
-    uint32_t there = 0;  // per stage two bits: which halves of the step hold keys
 #pragma unroll
-    for (int i = 0; i < S::STAGES - 1; ++i) {
-        const int s = s_begin + warp + i * kWarps;
-        const int page = page_next;
-        page_next = page_of(s + kWarps);
-        const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
-        there |= ((ok & 1u) | ((ok >> 15) & 2u)) << (2 * i);
-        issue(s, i, page);
-    }
-    int stage = 0;
-    for (int s = s_begin + warp; s < s_end; s += kWarps) {
-        {
-            const int sn = s + (S::STAGES - 1) * kWarps;
-            const int st = stage == 0 ? S::STAGES - 1 : stage - 1;
-            const int page = page_next;
-            page_next = page_of(sn + kWarps);
-            const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);  // every lane is past its reads of that stage
-            there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 15) & 2u)) << (2 * st));
-            issue(sn, st, page);
-        }
+    for (int i = 0; i < S::STAGES - 1; ++i) issue(i, i);
+    int stage = 0, turn = S::STAGES - 1;
+    for (int s = s_begin + warp; s < s_end; s += kWarps, ++turn) {
+        __syncwarp();  // every lane is past its reads of the stage that is filled next
+        issue(turn, stage == 0 ? S::STAGES - 1 : stage - 1);
         cp_wait<S::STAGES - 1>();
         __syncwarp();
         const uint8_t* st = ring + stage * S::STAGE;
-        const float* scales = reinterpret_cast<const float*>(st + 2 * kStep * S::ROW);
-        const int j0 = base + (s + (s >= range.head ? shift : 0)) * kStep;  // position of the step's first key
-        const uint32_t has = (there >> (2 * stage)) & 3u;
-        const bool all = has == 3u && j0 + kStep - 1 <= sure && (j0 > sure_low || j0 + kStep <= a.sinks);
+        const float4 kf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW)[(g & 1) * 4 + (g >> 1)];
+        const float4 vf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW + kStep * 4)[(g & 1) * 4 + (g >> 1)];
+        const bool all = (uint32_t)(s - sure_from) < sure_steps && !lost;
 
         // ---- scores
-        float x[2][NR][4], ks[2][2], vs[2][2];
+        float x[2][NR][4];
+        float ks[2][2] = {{kf.x * a.scale_log2, kf.y * a.scale_log2}, {kf.z * a.scale_log2, kf.w * a.scale_log2}};
+        float vs[2][2] = {{vf.x, vf.y}, {vf.z, vf.w}};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int row = c * 16 + (g & 1) * 4 + (g >> 1);  // key of product row g; row g + 8 is 8 further
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ks[c][e] = scales[row + 8 * e] * a.scale_log2;
-                vs[c][e] = scales[kStep + row + 8 * e];
-            }
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                x[c][n][0] = x[c][n][2] = start[n][0];
-                x[c][n][1] = x[c][n][3] = start[n][1];
-            }
             constexpr int KB = D >= 128 ? 16 : 8;  // bytes a read takes
 #pragma unroll
             for (int i = 0; i < S::KW * 4 / KB; ++i) {
@@ -335,7 +339,12 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t l0 = nib.lo(a0), l1 = nib.lo(a1), h0 = nib.hi72(a0), h1 = nib.hi72(a1);
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) mma16816(x[c][n], l0, l1, h0, h1, qf[n][k][2 * e], qf[n][k][2 * e + 1]);
+                        for (int n = 0; n < NR; ++n) {
+                            if (k == 0 && e == 0)
+                                mma16816_from(x[c][n], start[n][0], start[n][1], l0, l1, h0, h1, qf[n][k][0], qf[n][k][1]);
+                            else
+                                mma16816(x[c][n], l0, l1, h0, h1, qf[n][k][2 * e], qf[n][k][2 * e + 1]);
+                        }
                         a0 >>= 8, a1 >>= 8;
                     }
                 }
@@ -344,12 +353,14 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
         // Masked scores become -infinity (their scale, which may hold anything, is multiplied in first), and
         // what no row sees gets the value scale 0.
         if (!all) {
+            const int j0 = base + (s + (s >= range.head ? shift : 0)) * kStep;  // position of the step's first key
+            const float there[2][2] = {{kf.x, kf.y}, {kf.z, kf.w}};
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + c * 16 + (g & 1) * 4 + (g >> 1) + 8 * e;
-                    const bool in = ((has >> c) & 1u) && j - base < range.limit;
+                    const bool in = there[c][e] >= 0.0f && j - base < range.limit;
                     bool any = false;
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
@@ -368,7 +379,9 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
         // ---- weights, by the reference so far.  It is raised, and what is summed scaled down, only where a
         // weight would pass kMostWeight (or is no number: an overflow times a scale of 0); a vote
         // decides, so all lanes of a row agree.
-        float wt[2][NR][4], wv[2][NR][4];
+        float wt[2][NR][4];
+        __half2 wv[2][NR][2];
+        const __half2 most = __float2half2_rn(kMostWeight);
         auto weigh = [&]() {
             bool fits = true;
 #pragma unroll
@@ -376,10 +389,12 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wt[c][n][i] = ex2(__fmaf_rn(x[c][n][i], ks[c][i >> 1], -refl[n][i & 1]));
-                        wv[c][n][i] = wt[c][n][i] * vs[c][i >> 1];
-                        fits = fits && wv[c][n][i] <= kMostWeight;
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            wt[c][n][2 * e + q] = ex2(__fmaf_rn(x[c][n][2 * e + q], ks[c][e], -refl[n][q]));
+                        wv[c][n][e] = __floats2half2_rn(wt[c][n][2 * e] * vs[c][e], wt[c][n][2 * e + 1] * vs[c][e]);
+                        fits = fits && __hble2(wv[c][n][e], most);
                     }
             return fits;
         };
@@ -415,8 +430,7 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                 for (int e = 0; e < 2; ++e) {
                     sum[n][0] += wt[c][n][2 * e];
                     sum[n][1] += wt[c][n][2 * e + 1];
-                    const __half2 h2 = __floats2half2_rn(wv[c][n][2 * e], wv[c][n][2 * e + 1]);
-                    p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h2));
+                    p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&wv[c][n][e]));
                 }
             constexpr int VB = S::VW * 4;
             uint32_t v[4][S::VW];
@@ -441,7 +455,6 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
                     }
                 }
         }
-        __syncwarp();
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
@@ -501,14 +514,17 @@ __global__ void __launch_bounds__(32 * kWarps) stream_kernel(const AttentionArgs
     }
 }
 
-// Joins the partial results of a row: one block of kJoinWarps warps a row, each warp every
-// kJoinWarps-th slot, the slots' (M, L) read by all lanes at once; rows are dealt out as (sequence,
-// token, head).
-constexpr int kJoinWarps = 4;
+// Joins the partial results of a row, one block a row; rows are dealt out as (sequence, token, head).
+// All (M, L) are read at once and become weights in shared memory, then each warp sums every
+// kJoinWarps-th slot with four loads in flight: what it costs is the chain of loads, so the chain is
+// kept short (32 rows of 74 slots took 14.5 us with one load in flight and four warps).
+constexpr int kJoinWarps = 8;
+constexpr int kMostSlots = 4096;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionArgs a, const int slots) {
     constexpr int E = D / 32;
-    __shared__ float part[kJoinWarps][D], part_l[kJoinWarps];
+    extern __shared__ float weight[];
+    __shared__ float part[kJoinWarps][D], red[2][kJoinWarps];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -523,32 +539,47 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     const Parts p = parts(a, slots);
     const int64_t at = (token * a.q_heads + head) * slots;
     float M = kNone;
-    for (int k = lane; k < slots; k += 32) M = fmaxf(M, p.ml[at + k].x);
+    for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) M = fmaxf(M, p.ml[at + k].x);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[0][w]);
     float L = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int k0 = 0; k0 < slots; k0 += 32 * kJoinWarps) {
-        const int mine = k0 + warp + lane * kJoinWarps;
-        const float2 ml = mine < slots ? p.ml[at + mine] : make_float2(kNone, 0.0f);
+    for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) {
+        const float2 ml = p.ml[at + k];
         const float f = ml.y > 0.0f ? ex2(ml.x - M) : 0.0f;
+        weight[k] = f;
         L += f * ml.y;
-        uint32_t full = __ballot_sync(0xffffffffu, ml.y > 0.0f);
-        while (full) {
-            const int l = __ffs(full) - 1;
-            full &= full - 1;
-            const float w = __shfl_sync(0xffffffffu, f, l);
-            const float* src = p.o + (at + k0 + warp + l * kJoinWarps) * D + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(w, src[e], acc[e]);
-        }
     }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+    if (lane == 0) red[1][warp] = L;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    __syncthreads();
+    for (int k0 = warp; k0 < slots; k0 += 4 * kJoinWarps) {
+        float w[4], v[4][E];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * kJoinWarps;
+            w[u] = k < slots ? weight[k] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
+            if (w[u] > 0.0f) {  // an empty slot's O was never written
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<float2*>(&v[u][e]) = *reinterpret_cast<const float2*>(p.o + (at + k) * D + lane * E + e);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(w[u], v[u][e], acc[e]);
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-    if (lane == 0) part_l[warp] = L;
     __syncthreads();
     if (warp != 0) return;
     L = 0.0f;
@@ -556,7 +587,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        L += part_l[w];
+        L += red[1][w];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += part[w][lane * E + e];
     }
@@ -567,27 +598,32 @@ static Deal deal_out(const AttentionArgs& a, int rows) {
     const int G = a.q_heads / a.kv_heads;
     Deal d = {};
     d.own_tiles = (int)(((int64_t)a.max_q * G + rows - 1) / rows);
-    // Blocks enough for four turns of every SM's room, but no split under 512 keys (four steps a warp).
-    const int64_t want = getenv("QW") ? atoi(getenv("QW")) : 148 * 3 * 4, least = getenv("QL") ? atoi(getenv("QL")) : 16;
-    auto split = [&](int64_t blocks, int64_t keys, int* splits, int* chunk) {
+    // A split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths, at most 4096.
+    // Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by 8 kv heads
+    // took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the bound on
+    // their lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with one
+    // turn, 179 with two and 174 with four.
+    const bool equal = a.batch == 1 || a.window > 0;
+    const int64_t least = 16, most = equal ? 1 << 20 : 128;
+    auto split = [&](int64_t blocks, int64_t keys, int turns, int* splits, int* chunk) {
         const int64_t steps = (keys + kStep - 1) / kStep + 1;
-        int64_t n = (want + blocks - 1) / blocks;
-        n = std::max<int64_t>(1, std::min(n, steps / least));
+        int64_t n = turns * 592 / blocks;
+        n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
+        n = std::min<int64_t>(n, kMostSlots / 2);
         *chunk = (int)((steps + n - 1) / n);
         *splits = (int)((steps + *chunk - 1) / *chunk);
     };
     int64_t own = (int64_t)a.max_kv - a.prefix_len;
     int64_t shared = a.prefix_len;
     if (a.window) {
-        const int64_t most = (int64_t)a.window + a.max_q + a.sinks + 2 * kStep;
-        own = std::min(own, most);
+        own = std::min(own, (int64_t)a.window + a.max_q + a.sinks + 2 * kStep);
         // rows of the whole batch stand at positions far apart: no bound on what they see of the prefix
     }
     own = std::max<int64_t>(own, 1);
-    split((int64_t)a.batch * a.kv_heads * d.own_tiles, own, &d.own_splits, &d.own_chunk);
+    split((int64_t)a.batch * a.kv_heads * d.own_tiles, own, equal ? 1 : 2, &d.own_splits, &d.own_chunk);
     if (a.prefix_len) {
         d.prefix_tiles = (int)((a.tokens * G + rows - 1) / rows);
-        split((int64_t)a.kv_heads * d.prefix_tiles, shared, &d.prefix_splits, &d.prefix_chunk);
+        split((int64_t)a.kv_heads * d.prefix_tiles, shared, 1, &d.prefix_splits, &d.prefix_chunk);
     }
     d.slots = a.prefix_len || d.own_splits > 1 ? d.prefix_splits + d.own_splits : 0;
     return d;
@@ -612,7 +648,7 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
     if (e != cudaSuccess || d.slots == 0) return e;
     cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.max_q * a.q_heads));
     cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = d.slots * sizeof(float);
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, d.slots);
 }
 
