@@ -14,7 +14,7 @@
 extern "C" {
 #endif
 
-/* Give every on-chip wait of later tensor-core GEMM and one-token launches at most `cycles` SM
+/* Give every on-chip wait of later tensor-core GEMM, one-token and many-row attention launches at most `cycles` SM
  * clock cycles before it gives up (default about 4e9, some two seconds).  cycles <= 0 restores
  * the default.  Per host thread: it applies to the launches that thread makes. */
 qift_status qift_debug_set_wait_limit(int64_t cycles);
@@ -31,6 +31,13 @@ qift_status qift_debug_stall_next_gemm(void);
  * wait limit; every CTA then waits for its own copies to land and exits without writing its
  * outputs, and qift_device_error() reports QIFT_ERR_TIMEOUT.  One-shot, per host thread. */
 qift_status qift_debug_stall_next_one_token(void);
+
+/* Make the next launch of the attention kernel for many rows (qift_paged_attention with prompts, or
+ * with a prefix shared by many rows) wait, in the thread that issues its products, on a barrier that
+ * nothing ever arrives on.  That wait runs out after the wait limit; every role leaves its loop, tensor
+ * memory is freed, the rows are not written and qift_device_error() reports QIFT_ERR_TIMEOUT.
+ * One-shot, per host thread. */
+qift_status qift_debug_stall_next_attention(void);
 
 /* Turn programmatic dependent launch of the qift_linear and qift_decode_linear kernels on
  * (default) or off, to measure what the overlap with the previous kernel is worth.  Per host

@@ -538,3 +538,18 @@ def test_a_layer_prompt_then_single_tokens(window, sinks):
     # each side is off by at most the bound above; values are at most 7 * max scale
     assert (o_all.float() - o_parts).abs().max() <= 2 * (2.0 ** -11 + 2.0 ** -12 + 2e-3) * 7 * one[3][~one[3].isnan()].max()
     assert torch.isfinite(y_all).all() and y_all.shape == (T, n_in)
+
+
+def test_wait_that_runs_out_is_reported_and_the_context_survives():
+    m = make([200], [300], 8, 2, 128, 16, seed=20)
+    want = call(m)
+    assert qg.qift_device_error() == (qg.QIFT_OK, 0)
+    qg.qift_debug_set_wait_limit(20_000_000)               # about 10 ms a wait
+    qg.qift_debug_stall_next_attention()
+    call(m)
+    status, word = qg.qift_device_error()
+    qg.qift_debug_set_wait_limit(0)
+    assert status == qg.QIFT_ERR_TIMEOUT and word != 0
+    assert qg.qift_device_error() == (qg.QIFT_OK, 0)
+    assert torch.equal(call(m), want)
+    assert qg.qift_device_error() == (qg.QIFT_OK, 0)

@@ -66,6 +66,7 @@ def lib() -> C.CDLL:
         L.qift_debug_set_wait_limit.argtypes = [i64]
         L.qift_debug_stall_next_gemm.argtypes = []
         L.qift_debug_stall_next_one_token.argtypes = []
+        L.qift_debug_stall_next_attention.argtypes = []
         L.qift_debug_set_linear_path.argtypes = [i32]
         L.qift_debug_set_pdl.argtypes = [i32]
         L.qift_debug_check_line.argtypes = [C.POINTER(i32)]
@@ -79,7 +80,7 @@ def lib() -> C.CDLL:
                      "qift_linear", "qift_decode_linear",
                      "qift_append_kv", "qift_gather_kv", "qift_paged_attention",
                      "qift_device_error", "qift_debug_set_wait_limit", "qift_debug_stall_next_gemm",
-                     "qift_debug_stall_next_one_token",
+                     "qift_debug_stall_next_one_token", "qift_debug_stall_next_attention",
                      "qift_debug_set_linear_path", "qift_debug_set_pdl", "qift_debug_check_line"):
             getattr(L, name).restype = C.c_int
         _lib = L
@@ -586,6 +587,11 @@ def qift_debug_stall_next_gemm() -> None:
 def qift_debug_stall_next_one_token() -> None:
     """Test hook: the next one-token launch waits on a barrier nothing arrives on and times out."""
     _check(lib().qift_debug_stall_next_one_token(), "qift_debug_stall_next_one_token")
+
+
+def qift_debug_stall_next_attention() -> None:
+    """Test hook: the next attention launch for many rows waits on a barrier nothing arrives on and times out."""
+    _check(lib().qift_debug_stall_next_attention(), "qift_debug_stall_next_attention")
 
 
 LINEAR_PATHS = {"auto": 0, "gemv": 1, "skinny": 2, "gemm_pair": 6, "one_token": 7}

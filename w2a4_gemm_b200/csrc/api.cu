@@ -462,7 +462,9 @@ qift_status qift_device_error(void* stream, int32_t* detail) {
     int word = 0, word1 = 0;
     if (qift::read_and_clear_device_error(&word) != cudaSuccess) return QIFT_ERR_CUDA;
     if (qift::read_and_clear_one_token_error(&word1) != cudaSuccess) return QIFT_ERR_CUDA;
-    word |= word1;
+    int word2 = 0;
+    if (qift::read_and_clear_attention_error(&word2) != cudaSuccess) return QIFT_ERR_CUDA;
+    word |= word1 | word2;
     if (detail) *detail = word;
     if (word & 0x100) return QIFT_ERR_CUDA;  // a failed bounds check (checked build only)
     return word ? QIFT_ERR_TIMEOUT : QIFT_OK;
@@ -487,6 +489,7 @@ int32_t qift_debug_checked_build(void) {
 qift_status qift_debug_set_wait_limit(int64_t cycles) {
     qift::debug_set_gemm_wait_limit((long long)cycles);
     qift::debug_set_one_token_wait_limit((long long)cycles);
+    qift::debug_set_attention_wait_limit((long long)cycles);
     return QIFT_OK;
 }
 
@@ -510,6 +513,11 @@ qift_status qift_debug_stall_next_gemm(void) {
 
 qift_status qift_debug_stall_next_one_token(void) {
     qift::debug_stall_next_one_token();
+    return QIFT_OK;
+}
+
+qift_status qift_debug_stall_next_attention(void) {
+    qift::debug_stall_next_attention();
     return QIFT_OK;
 }
 

@@ -1,5 +1,5 @@
 // attention.cu -- qift_paged_attention: attention over the paged KV4 cache, for few rows a
-// sequence (decode), and the join of partial results.
+// sequence (decode), the join of partial results, and which kernel takes what.
 //
 // "Qift: Shift-Friendly No-Zero W2 Post-Training Quantization for Rotated W2A4/KV4 LLM
 // Inference" names KV4.  For a row (token at position p, query head) with the cache's rotated
@@ -60,32 +60,6 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Two two's-complement nibbles, 16 bits apart, as binary16: from bits 0-3 exactly, from bits 4-7
-// plus 72 (1 x 2^6 with the nibble, its sign bit flipped, above the last four bits), or exactly.
-// Mask and flip are one three-input operation each; it takes one immediate at most, so the constants
-// are kept in registers (given as immediates, the compiler makes two operations of it).
-struct Nibbles {
-    uint32_t mask_lo, mask_hi, one_lo, one_hi;
-    __device__ __forceinline__ Nibbles() {
-        asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask_lo));
-        asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask_hi));
-        asm volatile("mov.b32 %0, 0x64086408;" : "=r"(one_lo));
-        asm volatile("mov.b32 %0, 0x54805480;" : "=r"(one_hi));
-    }
-    __device__ __forceinline__ static uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) {
-        uint32_t r;
-        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(m), "r"(c));  // (w & m) ^ c
-        return r;
-    }
-    __device__ __forceinline__ uint32_t lo(uint32_t w) const { return sub2(and_xor(w, mask_lo, one_lo), one_lo); }
-    __device__ __forceinline__ uint32_t hi72(uint32_t w) const { return and_xor(w, mask_hi, one_hi); }
-    __device__ __forceinline__ uint32_t hi(uint32_t w) const { return sub2(hi72(w), one_hi); }
-};
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -117,17 +91,6 @@ __device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], const uint8_t* p) 
         r[0] = *reinterpret_cast<const uint32_t*>(p);
     }
 }
-
-// How the blocks of a launch are dealt out: first the prefix's (row tile, kv head, split), then each
-// sequence's.  A split is a run of `*_chunk` steps of kStep keys.
-struct Deal {
-    int prefix_tiles, prefix_splits, prefix_chunk;
-    int own_tiles, own_splits, own_chunk;
-    int slots;  // partial results a row has room for; 0: one split and no prefix, rows are finished at once
-    int64_t blocks(int batch, int kv_heads) const {
-        return (int64_t)kv_heads * ((int64_t)prefix_tiles * prefix_splits + (int64_t)batch * own_tiles * own_splits);
-    }
-};
 
 // Eight query rows are the columns of one product tile; NR of them a block.
 template <int D, int NR>
@@ -594,36 +557,55 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     finish_row<D>(a, acc, M, L, token, head, lane);
 }
 
-static Deal deal_out(const AttentionArgs& a, int rows) {
+// Rows a kv head from which a row set goes to the kernel for many rows.
+constexpr int64_t kWideFrom = 64;
+
+// Rows of a block of the streaming kernel: 8 where no row set it takes has more.
+static int stream_rows(const AttentionArgs& a) {
+    const int64_t G = a.q_heads / a.kv_heads;
+    return a.max_q * G <= 8 && (!a.prefix_len || a.tokens * G <= 8 || (a.head_dim <= 128 && a.tokens * G >= kWideFrom))
+               ? 8
+               : 16;
+}
+
+static Deal deal_out(const AttentionArgs& a) {
     const int G = a.q_heads / a.kv_heads;
+    const int64_t own_rows = (int64_t)a.max_q * G, shared_rows = a.tokens * G;
     Deal d = {};
-    d.own_tiles = (int)(((int64_t)a.max_q * G + rows - 1) / rows);
-    // A split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths, at most 4096.
-    // Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by 8 kv heads
-    // took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the bound on
-    // their lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with one
-    // turn, 179 with two and 174 with four.
+    d.own_wide = a.head_dim <= 128 && own_rows >= kWideFrom;
+    d.prefix_wide = a.head_dim <= 128 && shared_rows >= kWideFrom;
+    // The streaming kernel.  A split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths,
+    // at most 4096.  Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by
+    // 8 kv heads took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the
+    // bound on their lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with
+    // one turn, 179 with two and 174 with four.
+    // The kernel for many rows has one block an SM; it is split only where there are fewer row sets than SMs.
     const bool equal = a.batch == 1 || a.window > 0;
-    const int64_t least = 16, most = equal ? 1 << 20 : 128;
-    auto split = [&](int64_t blocks, int64_t keys, int turns, int* splits, int* chunk) {
-        const int64_t steps = (keys + kStep - 1) / kStep + 1;
-        int64_t n = turns * 592 / blocks;
+    auto split = [&](bool wide, int64_t blocks, int64_t keys, int turns, int* splits, int* chunk) {
+        const int64_t step = wide ? kWideStep : kStep;
+        const int64_t least = 512 / step, most = wide || equal ? 1 << 20 : 4096 / step;
+        const int64_t steps = (keys + step - 1) / step + 1;
+        int64_t n = wide ? 148 / blocks : turns * 592 / blocks;
         n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
         n = std::min<int64_t>(n, kMostSlots / 2);
         *chunk = (int)((steps + n - 1) / n);
         *splits = (int)((steps + *chunk - 1) / *chunk);
     };
+    auto tiles_of = [&](bool wide, int64_t rows) {
+        const int per = wide ? kWideRows : stream_rows(a);
+        return (int)((rows + per - 1) / per);
+    };
     int64_t own = (int64_t)a.max_kv - a.prefix_len;
-    int64_t shared = a.prefix_len;
     if (a.window) {
         own = std::min(own, (int64_t)a.window + a.max_q + a.sinks + 2 * kStep);
         // rows of the whole batch stand at positions far apart: no bound on what they see of the prefix
     }
     own = std::max<int64_t>(own, 1);
-    split((int64_t)a.batch * a.kv_heads * d.own_tiles, own, equal ? 1 : 2, &d.own_splits, &d.own_chunk);
+    d.own_tiles = tiles_of(d.own_wide, own_rows);
+    split(d.own_wide, (int64_t)a.batch * a.kv_heads * d.own_tiles, own, equal ? 1 : 2, &d.own_splits, &d.own_chunk);
     if (a.prefix_len) {
-        d.prefix_tiles = (int)((a.tokens * G + rows - 1) / rows);
-        split((int64_t)a.kv_heads * d.prefix_tiles, shared, 1, &d.prefix_splits, &d.prefix_chunk);
+        d.prefix_tiles = tiles_of(d.prefix_wide, shared_rows);
+        split(d.prefix_wide, (int64_t)a.kv_heads * d.prefix_tiles, a.prefix_len, 1, &d.prefix_splits, &d.prefix_chunk);
     }
     d.slots = a.prefix_len || d.own_splits > 1 ? d.prefix_splits + d.own_splits : 0;
     return d;
@@ -632,7 +614,7 @@ static Deal deal_out(const AttentionArgs& a, int rows) {
 template <int D, int NR>
 static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
     const size_t smem = Shape<D>::smem(NR);
-    cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
+    const cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)d.blocks(a.batch, a.kv_heads));
@@ -644,45 +626,57 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, stream_kernel<D, NR>, a, d);
-    if (e != cudaSuccess || d.slots == 0) return e;
-    cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.max_q * a.q_heads));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = d.slots * sizeof(float);
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, d.slots);
-}
-
-static int rows_per_block(const AttentionArgs& a) {
-    const int64_t G = a.q_heads / a.kv_heads;
-    const int64_t rows = std::max<int64_t>((int64_t)a.max_q * G, a.prefix_len ? a.tokens * G : 0);
-    return rows <= 8 ? 8 : 16;
+    return cudaLaunchKernelEx(&cfg, stream_kernel<D, NR>, a, d);
 }
 
 template <int D>
-static cudaError_t launch_rows_of(const AttentionArgs& a, cudaStream_t s) {
-    const int rows = rows_per_block(a);
-    const Deal d = deal_out(a, rows);
-    return rows == 8 ? launch_stream<D, 1>(a, d, s) : launch_stream<D, 2>(a, d, s);
+static cudaError_t launch_join(const AttentionArgs& a, int slots, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.max_q * a.q_heads));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = slots * sizeof(float);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, slots);
+}
+
+template <int D>
+static cudaError_t launch_all(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
+    for (const bool wide : {true, false}) {  // one launch for each kernel that has rows to do
+        Deal part = d;
+        if (d.prefix_wide != wide) part.prefix_tiles = 0;
+        if (d.own_wide != wide) part.own_tiles = 0;
+        if (part.blocks(a.batch, a.kv_heads) == 0) continue;
+        const cudaError_t e = wide                  ? launch_wide(a, part, s)
+                              : stream_rows(a) == 8 ? launch_stream<D, 1>(a, part, s)
+                                                    : launch_stream<D, 2>(a, part, s);
+        if (e != cudaSuccess) return e;
+    }
+    return d.slots ? launch_join<D>(a, d.slots, s) : cudaSuccess;
 }
 
 }  // namespace attn
 
 bool attention_supported(const AttentionArgs& a) {
-    const attn::Deal d = attn::deal_out(a, attn::rows_per_block(a));
+    const attn::Deal d = attn::deal_out(a);
     return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads <= 0x7fffffff;
 }
 
 int64_t attention_workspace_bytes(const AttentionArgs& a) {
-    const attn::Deal d = attn::deal_out(a, attn::rows_per_block(a));
-    return a.tokens * a.q_heads * d.slots * (a.head_dim + 2) * 4;
+    return a.tokens * a.q_heads * attn::deal_out(a).slots * (a.head_dim + 2) * 4;
 }
 
 cudaError_t launch_attention(AttentionArgs a, cudaStream_t s) {
     a.norm = a.block ? (float)(1.0 / sqrt((double)a.block)) : 1.0f;
+    const attn::Deal d = attn::deal_out(a);
     switch (a.head_dim) {
-        case 64: return attn::launch_rows_of<64>(a, s);
-        case 128: return attn::launch_rows_of<128>(a, s);
-        case 256: return attn::launch_rows_of<256>(a, s);
+        case 64: return attn::launch_all<64>(a, d, s);
+        case 128: return attn::launch_all<128>(a, d, s);
+        case 256: return attn::launch_all<256>(a, d, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -111,6 +111,48 @@ __device__ __forceinline__ Range visible(const AttentionArgs& a, int pmin, int p
     return r;
 }
 
+// How the blocks of a launch are dealt out: first the prefix's (row tile, kv head, split), then each
+// sequence's.  A split is a run of `*_chunk` steps of the kernel's key blocks.  The two kinds may go to
+// different kernels; the launch of one then has no tiles of the other kind.
+struct Deal {
+    int prefix_tiles, prefix_splits, prefix_chunk;
+    int own_tiles, own_splits, own_chunk;
+    int slots;  // partial results a row has room for; 0: one split and no prefix, rows are finished at once
+    bool prefix_wide, own_wide;  // whether the kernel for many rows takes them
+    int64_t blocks(int batch, int kv_heads) const {
+        return (int64_t)kv_heads * ((int64_t)prefix_tiles * prefix_splits + (int64_t)batch * own_tiles * own_splits);
+    }
+};
+cudaError_t launch_wide(const AttentionArgs& a, const Deal& d, cudaStream_t s);
+constexpr int kWideRows = 256;  // rows of a block of the kernel for many rows
+constexpr int kWideStep = 128;  // keys it takes at a time
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two two's-complement nibbles, 16 bits apart, as binary16: from bits 0-3 exactly, from bits 4-7
+// plus 72 (1 x 2^6 with the nibble, its sign bit flipped, above the last four bits), or exactly.
+// Mask and flip are one three-input operation each; it takes one immediate at most, so the constants
+// are kept in registers (given as immediates, the compiler makes two operations of it).
+struct Nibbles {
+    uint32_t mask_lo, mask_hi, one_lo, one_hi;
+    __device__ __forceinline__ Nibbles() {
+        asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask_lo));
+        asm volatile("mov.b32 %0, 0x00F000F0;" : "=r"(mask_hi));
+        asm volatile("mov.b32 %0, 0x64086408;" : "=r"(one_lo));
+        asm volatile("mov.b32 %0, 0x54805480;" : "=r"(one_hi));
+    }
+    __device__ __forceinline__ static uint32_t and_xor(uint32_t w, uint32_t m, uint32_t c) {
+        uint32_t r;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(m), "r"(c));  // (w & m) ^ c
+        return r;
+    }
+    __device__ __forceinline__ uint32_t lo(uint32_t w) const { return sub2(and_xor(w, mask_lo, one_lo), one_lo); }
+    __device__ __forceinline__ uint32_t hi72(uint32_t w) const { return and_xor(w, mask_hi, one_hi); }
+    __device__ __forceinline__ uint32_t hi(uint32_t w) const { return sub2(hi72(w), one_hi); }
+};
+
 // Partial results: slot p of row (token, head): D floats of O and (M, L).
 struct Parts {
     float* o;

@@ -1,0 +1,660 @@
+// attention_wide.cu -- qift_paged_attention for many rows a kv head (prompts, and the shared prefix
+// of a whole batch), on the sm_100a tensor cores (tcgen05).
+//
+// "Qift: Shift-Friendly No-Zero W2 Post-Training Quantization for Rotated W2A4/KV4 LLM
+// Inference" names KV4.  The formula is attention.cu's.  A block takes two tiles of 128 rows against
+// the same keys, 128 at a time:
+//   S = Q K^T   (binary16 x binary16 -> fp32 in tensor memory)
+//   p_j = 2^(scale s_j S_j - ref) t_j, rounded to binary16 into tensor memory over S
+//   O += P V    (P from tensor memory, O stays there)
+// K and V come from the paged 4-bit cache: four warps read the codes into registers (a step ahead) and
+// write them as exact whole numbers in binary16 in the layout the tensor core reads: K rows of keys,
+// V transposed (rows of values, so that both operands are contiguous along the sum), 128-byte swizzled.
+// The scales stay apart in fp32, so no rounding is added.  The order of values inside each group of
+// eight is that in which a word's nibbles come out; Q is laid out alike.
+//
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
+//   warps 8-11       unpack K, V; copy the scales
+//   warp 12          tensor-memory owner and issuer of the products (13-15 fill its register group)
+// Tile 1's products run while tile 0's softmax does, and the other way round.
+//
+// A row's reference is raised (and O scaled down) only when the weights of a step would not fit
+// binary16: the test is the step's sum of 2^u times its largest t_j, so it costs one product a row.
+//
+// Every wait is bounded: one that runs out sets a shared abort flag and the device error word, every
+// role leaves its loop, the products in flight are waited for and tensor memory is freed.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "tc.cuh"
+
+namespace qift {
+namespace attn {
+namespace wide {
+
+__device__ int g_error = 0;  // bit 1: a wait ran out (read by qift_device_error)
+
+constexpr int BM = 128, BN = kWideStep, TILES = 2, STAGES = 2, RING = 4;
+static_assert(BM * TILES == kWideRows, "rows of a block");
+constexpr int kSoftWarps = 4 * TILES, kUnpackWarps = 4;
+constexpr int kUnpackThreads = 32 * kUnpackWarps;
+// Four groups of four warps, launched with 128 registers a thread and redistributed: a softmax thread holds a
+// row's 128 weights in pairs.  The shares sum to the four groups' 4 x 128.
+constexpr int kThreads = 32 * (kSoftWarps + kUnpackWarps + 4);
+constexpr int kSoftRegs = 176, kUnpackRegs = 104, kIssueRegs = 56;
+static_assert(TILES == 2 && 2 * kSoftRegs + kUnpackRegs + kIssueRegs == 4 * 128, "registers of the launch");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLift = 4.0f, kMostWeight = 32768.0f;
+constexpr uint32_t kNowhere = 0xffffffffu;
+
+constexpr long long kWaitCycles = 4000000000LL;  // ~2 s before a wait gives up
+static thread_local long long g_wait_limit = kWaitCycles;
+static thread_local bool g_stall_next = false;
+
+template <int D>
+struct Shape {
+    static constexpr int CB = D / 64;                    // 128-byte columns of a row of Q or K
+    static constexpr int ROW = D / 2;                    // bytes of a row of codes
+    static constexpr int CH = D / 32;                    // 16-byte pieces of it
+    static constexpr int VB = D == 64 ? 4 : 8;           // bytes of a value row that a thread transposes
+    static constexpr int Q_BYTES = BM * D * 2, K_BYTES = BN * D * 2, V_BYTES = BN * D * 2;
+    static constexpr int K_AT = TILES * Q_BYTES, V_AT = K_AT + STAGES * K_BYTES, SC_AT = V_AT + STAGES * V_BYTES;
+    static constexpr int BAR_AT = SC_AT + RING * (BN * 8 + 32);
+    static constexpr int SMEM = BAR_AT + 256 + 1024;
+    static constexpr int OPAD = D + 4;
+    static_assert(TILES * BM * OPAD * 4 <= BAR_AT, "finished rows lie over the operands");
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(2 * BN + TILES * D <= (int)kTmemCols, "tensor memory");
+};
+
+struct Bars {
+    uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
+    uint64_t scales[RING];
+    uint64_t s_full[TILES], p_full[TILES], o_done[TILES];
+    uint64_t done, never;
+    uint32_t tmem;
+    int abort;
+    int pmin[TILES], pmax[TILES], least[TILES];
+};
+static_assert(sizeof(Bars) <= 256, "barrier area");
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort, long long limit) {
+    if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait_bounded(bar, parity, abort, limit)) return true;
+    if (!*reinterpret_cast<volatile int*>(abort)) {
+        atomicOr(&g_error, 1);
+        *reinterpret_cast<volatile int*>(abort) = 1;
+    }
+    return false;
+}
+
+// kind::f16, A and B binary16, fp32 accumulate, both operands contiguous along the sum.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        : "memory");
+}
+
+// Two fp32 at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
+
+// What a softmax thread knows of its row's view of a step, where not every row sees every key.
+struct View {
+    int hi, lo, sinks;   // key j counts if j <= hi and (j > lo or j < sinks)
+    int j0;              // position of the step's first key
+    uint32_t gone;       // 16s of keys that are not there
+    __device__ __forceinline__ bool sees(int k) const {
+        const int j = j0 + k;
+        return j <= hi && (j > lo || j < sinks) && !((gone >> (k >> 4)) & 1u);
+    }
+};
+
+// Weights of one step: S of this thread's row from tensor memory, p (binary16 pairs) and the sum of 2^u.
+template <bool MASK>
+__device__ __forceinline__ float weigh(uint32_t taddr, const float4* __restrict__ sc, float ref, const View& view,
+                                       uint32_t (&p)[BN / 2]) {
+    uint64_t sum = pack2(0.0f, 0.0f);
+    const uint64_t neg = pack2(-ref, -ref);
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) {
+        uint32_t x[32];
+        tc::tmem_ld_32x32b_x32(taddr + 32 * c, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float4 f = sc[c * 16 + e];
+            float u0, u1, p0, p1;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), pack2(f.x, f.y), neg), u0, u1);
+            bool s0 = true, s1 = true;
+            if (MASK) {
+                s0 = view.sees(c * 32 + 2 * e), s1 = view.sees(c * 32 + 2 * e + 1);
+                u0 = s0 ? u0 : -INFINITY, u1 = s1 ? u1 : -INFINITY;
+            }
+            const uint64_t w = pack2(ex2(u0), ex2(u1));
+            sum = add2(sum, w);
+            unpack2(mul2(w, pack2(f.z, f.w)), p0, p1);
+            if (MASK) p0 = s0 ? p0 : 0.0f, p1 = s1 ? p1 : 0.0f;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            p[c * 16 + e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    float s0, s1;
+    unpack2(sum, s0, s1);
+    return s0 + s1;
+}
+
+// The largest u_j + log2 t_j of a step.
+__device__ __forceinline__ float largest(uint32_t taddr, const float4* sc, const View& view, bool mask) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < BN / 16; ++c) {
+        uint32_t x[16];
+        tc::tmem_ld_32x32b_x16(taddr + 16 * c, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 f = sc[c * 8 + e];
+            const float u0 = __fmaf_rn(__uint_as_float(x[2 * e]), f.x, fmaxf(lg2(f.z), -28.0f));  // scales are 2^-24 / 7 or more
+            const float u1 = __fmaf_rn(__uint_as_float(x[2 * e + 1]), f.y, fmaxf(lg2(f.w), -28.0f));
+            if (!mask || view.sees(c * 16 + 2 * e)) top = fmaxf(top, u0);
+            if (!mask || view.sees(c * 16 + 2 * e + 1)) top = fmaxf(top, u1);
+        }
+    }
+    return top;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    wide_kernel(const AttentionArgs a, const Deal deal, long long limit, int stall) {
+    using S = Shape<D>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Bars& bar = *reinterpret_cast<Bars*>(smem + S::BAR_AT);
+    float4* scales = reinterpret_cast<float4*>(smem + S::SC_AT);                 // [RING][BN / 2]: two keys' s, two keys' t
+    float* v_most = reinterpret_cast<float*>(smem + S::SC_AT + RING * BN * 8);   // [RING][4]
+    uint32_t* gone = reinterpret_cast<uint32_t*>(v_most + RING * 4);             // [RING]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.q_heads / a.kv_heads;
+
+    // ---- which rows and keys
+    int64_t id = blockIdx.x;
+    const int64_t prefix_blocks = (int64_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
+    const bool prefix = id < prefix_blocks;
+    if (!prefix) id -= prefix_blocks;
+    const int splits = prefix ? deal.prefix_splits : deal.own_splits;
+    const int tiles = prefix ? deal.prefix_tiles : deal.own_tiles;
+    const int split = (int)(id % splits);
+    id /= splits;
+    const int h = (int)(id % a.kv_heads);
+    id /= a.kv_heads;
+    const int pair = tiles - 1 - (int)(id % tiles);  // the last rows see the most keys: they start first
+    const int b = (int)(id / tiles);                 // own only
+    const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
+    const int base = prefix ? 0 : a.prefix_len;
+    const int64_t capacity = prefix ? a.prefix_len : (int64_t)a.max_pages << a.log_page;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            tc::mbar_init(&bar.k_full[i], kUnpackThreads);
+            tc::mbar_init(&bar.k_empty[i], 1);
+            tc::mbar_init(&bar.v_full[i], kUnpackThreads);
+            tc::mbar_init(&bar.v_empty[i], 1);
+        }
+        for (int i = 0; i < RING; ++i) tc::mbar_init(&bar.scales[i], kUnpackThreads);
+        for (int i = 0; i < TILES; ++i) {
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.p_full[i], BM);
+            tc::mbar_init(&bar.o_done[i], 1);
+            bar.pmin[i] = bar.least[i] = 0x7fffffff;
+            bar.pmax[i] = -1;
+        }
+        tc::mbar_init(&bar.done, 1);
+        tc::mbar_init(&bar.never, 1);
+        bar.abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == kSoftWarps + kUnpackWarps) {
+        tc::tmem_alloc(&bar.tmem, kTmemCols);
+        tc::tmem_relinquish();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+
+    // ---- rows: position, and Q into shared memory
+    const int tile = warp >> 2, r = (warp & 3) * 32 + lane;  // of a softmax thread
+    int64_t token = -1;
+    int pos = -1, head = 0;
+    if (warp < kSoftWarps) {
+        const int64_t row = ((int64_t)pair * TILES + tile) * BM + r;
+        if (prefix) {
+            if (row < a.tokens * G) token = row / G, pos = position_of(a, token);
+        } else {
+            const Sequence s = sequence(a, b);
+            if (row < (int64_t)s.q_len * G) {
+                token = s.first + row / G;
+                const int p = s.kv_len - s.q_len + (int)(row / G);
+                pos = p < 0 ? -1 : p;
+            }
+        }
+        if (token >= a.tokens || token < 0) token = -1;
+        head = h * G + (int)(row % G);
+        if (token >= 0) {
+            atomicMin(&bar.least[tile], pos);
+            if (pos >= 0) atomicMin(&bar.pmin[tile], pos), atomicMax(&bar.pmax[tile], pos);
+        }
+        const __half* src = a.q + (token >= 0 ? token * a.q_stride + (int64_t)head * D : 0);
+        const uint32_t dst = tc::smem_u32(smem) + tile * S::Q_BYTES + r * 128;
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (token >= 0) x = *reinterpret_cast<const uint4*>(src + c * 8);
+            sts128(dst + (c >> 3) * (BM * 128) + (((c & 7) ^ (r & 7)) << 4), prmt(x.x, x.z, 0x5410u),
+                   prmt(x.x, x.z, 0x7632u), prmt(x.y, x.w, 0x5410u), prmt(x.y, x.w, 0x7632u));
+        }
+        tc::fence_proxy_async_smem();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int pmax = max(bar.pmax[0], bar.pmax[1]);
+    Range range = {0, 0, 0, 0};
+    if (pmax >= 0) range = visible<BN>(a, min(bar.pmin[0], bar.pmin[1]), pmax, base, capacity);
+    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
+    const int s_begin = min(split * chunk, range.steps), n = min(chunk, range.steps - s_begin);
+    const int shift = range.main - range.head;
+    auto block_of = [&](int i) { return s_begin + i + (s_begin + i >= range.head ? shift : 0); };
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------------------------------------ softmax
+        more_registers<kSoftRegs>();
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + quarter + tile * BN, t_o = tmem + quarter + 2 * BN + tile * D;
+        const int t_least = bar.least[tile], t_pmax = bar.pmax[tile];
+        float ref = kNone, sum = 0.0f;
+        View view;
+        view.hi = min(pos, base + range.limit - 1);
+        view.lo = a.window ? pos - a.window : -1;
+        view.sinks = a.sinks;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int ring = i % RING;
+            ok = wait(&bar.scales[ring], (i / RING) & 1, &bar.abort, limit) &&
+                 wait(&bar.s_full[tile], i & 1, &bar.abort, limit);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const float4* sc = scales + ring * (BN / 2);
+            const float4 m4 = reinterpret_cast<const float4*>(v_most)[ring];
+            const float most = kMostWeight / fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), 0x1p-28f);
+            view.j0 = base + block_of(i) * BN;
+            view.gone = gone[ring];
+            const bool mask = !(view.j0 + BN - 1 <= t_least && view.j0 + BN <= base + range.limit && view.gone == 0 &&
+                                (!a.window || view.j0 > t_pmax - a.window || view.j0 + BN <= a.sinks));
+            uint32_t p[BN / 2];
+            float part = mask ? weigh<true>(t_s, sc, ref, view, p) : weigh<false>(t_s, sc, ref, view, p);
+            if (!__all_sync(0xffffffffu, part <= most)) {  // also where it is no number
+                const float to = fmaxf(ref, largest(t_s, sc, view, mask) - kLift);
+                const float down = ex2(ref - to);
+                ref = to;
+                sum *= down;
+                if (i > 0) {
+                    ok = __all_sync(0xffffffffu, wait(&bar.o_done[tile], (i - 1) & 1, &bar.abort, limit));
+                    if (!ok) break;
+                    tc::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t x[16];
+                        tc::tmem_ld_32x32b_x16(t_o + 16 * c, x);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * down);
+                        asm volatile(
+                            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+                            "%14,%15,%16};" ::"r"(t_o + 16 * c),
+                            "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
+                            "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+                            : "memory");
+                    }
+                    tc::tmem_st_wait();
+                }
+                part = mask ? weigh<true>(t_s, sc, ref, view, p) : weigh<false>(t_s, sc, ref, view, p);
+            }
+            sum += part;
+            uint32_t half[32];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) half[e] = p[32 * k + e];
+                tc::tmem_st_32x32b_x32(t_s + 32 * k, half);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bar.p_full[tile]);
+        }
+        if (n > 0 && ok) ok = wait(&bar.o_done[tile], (n - 1) & 1, &bar.abort, limit);
+        ok = __all_sync(0xffffffffu, ok);
+        soft_bar();  // both tiles' products are done: the operands' memory is free
+        // Rows through shared memory, so that a warp finishes one together (rotation back, whole lines).
+        ok = ok && !*reinterpret_cast<volatile int*>(&bar.abort);
+        if (ok) {
+            tc::tc_fence_after();
+            float* rows = reinterpret_cast<float*>(smem) + (tile * BM + (warp & 3) * 32) * S::OPAD;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                if (n > 0) {
+                    tc::tmem_ld_32x32b_x32(t_o + 32 * c, x);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4*>(rows + lane * S::OPAD + 32 * c + e) =
+                        make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+            __syncwarp();
+            constexpr int E = D / 32;
+            for (int k = 0; k < 32; ++k) {
+                const int64_t tk = __shfl_sync(0xffffffffu, token, k);
+                const int hd = __shfl_sync(0xffffffffu, head, k);
+                const float M = __shfl_sync(0xffffffffu, ref, k), L = __shfl_sync(0xffffffffu, sum, k);
+                if (tk < 0) continue;
+                float acc[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = rows[k * S::OPAD + lane * E + e];
+                if (deal.slots == 0) {
+                    finish_row<D>(a, acc, M, L, tk, hd, lane);
+                } else {
+                    const Parts p = parts(a, deal.slots);
+                    const int64_t at = (tk * a.q_heads + hd) * deal.slots + (prefix ? split : deal.prefix_splits + split);
+                    if (lane == 0) p.ml[at] = make_float2(M, L);
+                    if (L > 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) p.o[at * D + lane * E + e] = acc[e];
+                    }
+                }
+            }
+        }
+    } else if (warp < kSoftWarps + kUnpackWarps) {
+        // ------------------------------------------------------------------------------- unpack
+        fewer_registers<kUnpackRegs>();
+        // A warp's lanes 0-7 hold where the step's eight 16s of keys lie in the pool.
+        const int w = warp - kSoftWarps, l8 = lane & 7, l4 = lane >> 3, u = w * 32 + lane;
+        const Nibbles nib;
+        auto find = [&](int i) -> uint32_t {
+            uint32_t at = kNowhere;
+            if (i < n && lane < 8) {
+                const int j = block_of(i) * BN + lane * 16;
+                if (j < range.limit) {
+                    const int page = table[j >> a.log_page];
+                    if ((uint32_t)page < (uint64_t)a.n_pages)
+                        at = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & ((1 << a.log_page) - 1))) >> 4);
+                }
+            }
+            return at;
+        };
+        uint4 kq[S::CH];
+        uint2 vq[8];
+        float ks, vs;
+        auto row_at = [&](uint32_t place, int kg) { return (uint64_t)place * 16 + (kg & 1) * 8; };
+        auto load_k = [&](uint32_t places, int i) {
+#pragma unroll
+            for (int q = 0; q < S::CH; ++q) {
+                const int v = (w * S::CH + q) * 4 + l4, kg = v / S::CH, cc = v % S::CH;
+                const uint32_t place = __shfl_sync(0xffffffffu, places, kg >> 1);
+                kq[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (place != kNowhere && QIFT_CK((int64_t)place * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page))
+                    kq[q] = __ldg(reinterpret_cast<const uint4*>(a.k_cache + (row_at(place, kg) + l8) * S::ROW + cc * 16));
+            }
+            const uint32_t place = __shfl_sync(0xffffffffu, places, u >> 4);
+            ks = vs = 0.0f;
+            if (place != kNowhere && block_of(i) * BN + u < range.limit) {
+                ks = __ldg(a.k_scales + (uint64_t)place * 16 + (u & 15)) * a.scale_log2;
+                vs = __ldg(a.v_scales + (uint64_t)place * 16 + (u & 15));
+            }
+        };
+        const int v_kg = l8 + 8 * (w & 1), v_dc = l4 + 4 * (w >> 1);  // eight keys, VB bytes of each
+        auto load_v = [&](uint32_t places) {
+            const uint32_t place = __shfl_sync(0xffffffffu, places, v_kg >> 1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                vq[j] = make_uint2(0u, 0u);
+                if (place != kNowhere && QIFT_CK((int64_t)place * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page)) {
+                    const uint8_t* p = a.v_cache + (row_at(place, v_kg) + j) * S::ROW + v_dc * S::VB;
+                    if constexpr (S::VB == 8) vq[j] = __ldg(reinterpret_cast<const uint2*>(p));
+                    else vq[j].x = __ldg(reinterpret_cast<const uint32_t*>(p));
+                }
+            }
+        };
+        uint32_t now = find(0), next = find(1);
+        load_k(now, 0);
+        load_v(now);
+        for (int i = 0; i < n; ++i) {
+            const int st = i % STAGES, ring = i % RING;
+            if (i >= STAGES &&
+                !__all_sync(0xffffffffu, wait(&bar.k_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
+                break;
+            // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free
+            float* sc = reinterpret_cast<float*>(scales + ring * (BN / 2) + (u >> 1)) + (u & 1);
+            sc[0] = ks;
+            sc[2] = vs;
+            float top = vs;
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            if (lane == 0) v_most[ring * 4 + w] = top;
+            const uint32_t away = __ballot_sync(0xffffffffu, lane < 8 && now == kNowhere);
+            if (u == 0) gone[ring] = away;
+            tc::mbar_arrive(&bar.scales[ring]);
+            const uint32_t k_to = tc::smem_u32(smem + S::K_AT + st * S::K_BYTES);
+#pragma unroll
+            for (int q = 0; q < S::CH; ++q) {
+                const int v = (w * S::CH + q) * 4 + l4, kg = v / S::CH, cc = v % S::CH;
+                const uint32_t words[4] = {kq[q].x, kq[q].y, kq[q].z, kq[q].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = cc * 4 + e;  // which group of eight values
+                    const uint32_t x = words[e], y = words[e] >> 8;
+                    sts128(k_to + (c >> 3) * (BN * 128) + (kg * 8 + l8) * 128 + (((c & 7) ^ l8) << 4), nib.lo(x), nib.hi(x),
+                           nib.lo(y), nib.hi(y));
+                }
+            }
+            if (i + 1 < n) load_k(next, i + 1);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&bar.k_full[st]);
+            if (i >= STAGES &&
+                !__all_sync(0xffffffffu, wait(&bar.v_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
+                break;
+            const uint32_t v_to = tc::smem_u32(smem + S::V_AT + st * S::V_BYTES) + (v_kg >> 3) * (D * 128);
+#pragma unroll
+            for (int wd = 0; wd < S::VB / 4; ++wd)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] = prmt(wd ? vq[2 * k].y : vq[2 * k].x, wd ? vq[2 * k + 1].y : vq[2 * k + 1].x,
+                                    hf ? 0x7632u : 0x5410u);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int d8 = 4 * hf + 2 * e;  // value's place among the word's eight
+                        const uint32_t to = v_to + (v_dc * (2 * S::VB) + wd * 8 + d8) * 128;
+                        sts128(to + (((v_kg & 7) ^ d8) << 4), nib.lo(x[0]), nib.lo(x[1]), nib.lo(x[2]), nib.lo(x[3]));
+                        sts128(to + 128 + (((v_kg & 7) ^ (d8 + 1)) << 4), nib.hi(x[0]), nib.hi(x[1]), nib.hi(x[2]),
+                               nib.hi(x[3]));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] >>= 8;
+                    }
+                }
+            if (i + 1 < n) load_v(next);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&bar.v_full[st]);
+            now = next;
+            next = find(i + 2);
+        }
+    } else {
+        fewer_registers<kIssueRegs>();
+        // ----------------------------------------------------------------------------- products
+        // S of a step follows only when the tile's P V before it is complete, since P lies over S; the
+        // other tile's products fill the time.
+        constexpr uint32_t id_s = idesc_f16(BM, BN), id_o = idesc_f16(BM, D);
+        const uint64_t q0 = tc::smem_desc_sw128(tc::smem_u32(smem));
+        const uint64_t k0 = tc::smem_desc_sw128(tc::smem_u32(smem + S::K_AT));
+        const uint64_t v0 = tc::smem_desc_sw128(tc::smem_u32(smem + S::V_AT));
+        const bool issuer = warp == kSoftWarps + kUnpackWarps && lane == 0;
+        auto product_s = [&](int t, int st) {
+#pragma unroll
+            for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ss(tmem + t * BN, q0 + (uint64_t)((t * S::Q_BYTES + c * BM * 128) >> 4) + 2 * k,
+                               k0 + (uint64_t)((st * S::K_BYTES + c * BN * 128) >> 4) + 2 * k, id_s, c + k != 0);
+            tc::mma_commit(&bar.s_full[t]);
+        };
+        bool ok = issuer;
+        if (stall && issuer) ok = wait(&bar.never, 0, &bar.abort, limit);  // test hook
+        if (n > 0 && issuer) {
+            ok = ok && wait(&bar.k_full[0], 0, &bar.abort, limit);
+            if (ok) {
+                tc::tc_fence_after();
+                for (int t = 0; t < TILES; ++t) product_s(t, 0);
+                tc::mma_commit(&bar.k_empty[0]);
+            }
+        }
+        for (int i = 0; ok && i < n; ++i) {
+            const int st = i % STAGES, sn = (i + 1) % STAGES;
+            ok = wait(&bar.v_full[st], (i / STAGES) & 1, &bar.abort, limit);
+            for (int t = 0; ok && t < TILES; ++t) {
+                ok = wait(&bar.p_full[t], i & 1, &bar.abort, limit);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    mma_f16_ts(tmem + 2 * BN + t * D, tmem + t * BN + k * 8,
+                               v0 + (uint64_t)((st * S::V_BYTES + (k >> 2) * D * 128) >> 4) + 2 * (k & 3), id_o,
+                               (i | k) != 0);
+                tc::mma_commit(&bar.o_done[t]);
+                if (t == TILES - 1) tc::mma_commit(&bar.v_empty[st]);
+                if (i + 1 < n) {
+                    ok = (t > 0 || wait(&bar.k_full[sn], ((i + 1) / STAGES) & 1, &bar.abort, limit)) &&
+                         wait(&bar.o_done[t], i & 1, &bar.abort, limit);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    product_s(t, sn);
+                    if (t == TILES - 1) tc::mma_commit(&bar.k_empty[sn]);
+                }
+            }
+        }
+        // Nothing may still read this block's memory when it leaves, also after an abort.
+        if (issuer) {
+            tc::mma_commit(&bar.done);
+            int zero = 0;
+            tc::mbar_wait_bounded(&bar.done, 0, &zero, limit);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps + kUnpackWarps) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+static cudaError_t launch_t(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
+    const cudaError_t e = ensure_smem(wide_kernel<D>, Shape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int stall = g_stall_next ? 1 : 0;
+    g_stall_next = false;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)d.blocks(a.batch, a.kv_heads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<D>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, wide_kernel<D>, a, d, g_wait_limit, stall);
+}
+
+}  // namespace wide
+
+cudaError_t launch_wide(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
+    if (a.head_dim == 64) return wide::launch_t<64>(a, d, s);
+    return wide::launch_t<128>(a, d, s);
+}
+
+}  // namespace attn
+
+void debug_set_attention_wait_limit(long long cycles) {
+    attn::wide::g_wait_limit = cycles > 0 ? cycles : attn::wide::kWaitCycles;
+}
+void debug_stall_next_attention() { attn::wide::g_stall_next = true; }
+
+cudaError_t read_and_clear_attention_error(int* word) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, attn::wide::g_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    if (v != 0) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(attn::wide::g_error, &zero, sizeof(int));
+    }
+    *word = v;
+    return e;
+}
+
+}  // namespace qift

@@ -163,6 +163,9 @@ struct AttentionArgs {
 bool attention_supported(const AttentionArgs& a);
 int64_t attention_workspace_bytes(const AttentionArgs& a);
 cudaError_t launch_attention(AttentionArgs a, cudaStream_t s);
+void debug_set_attention_wait_limit(long long cycles);
+void debug_stall_next_attention();
+cudaError_t read_and_clear_attention_error(int* word);
 
 // Test hooks behind qift_debug.h (numbers 3 to 5 named GEMM forms that are no longer built).
 enum LinearPath {
