@@ -8,6 +8,10 @@ A = sum_j w_j |v_j|:
   * a score's error e_u moves the weights by at most 2 e_u relative: the product adds D + D/2 * 72-fold values in
     groups of 16, each addition off by at most 2^-22 of partial sums that stay under 80 sum|q|, so
     e_u <= (D/16 + 1) 2^-22 80 sum|q| max_j s_j scale; the 2^u, scalings and sums add under 2^-17 relative;
+  * where a kv head has 64 rows or more (WIDE: prompts, a prefix that many rows share; head_dim up to 128), keys and
+    values are binary16 products of the code and the row's magnitude: 2^-12 of each more, so A grows by 2^-12 A (and
+    what lies under 2^-14 of the largest value of its 32 keys by 2^-25 of that), and a score is off by up to
+    2^-12 sum|q_d k_d| scale <= 2^-12 sum|q| 7 max s scale more;
   * a binary16 result is off by 2^-11 of the value (2^-25 where it is subnormal).
 """
 import math
@@ -219,6 +223,7 @@ def reference(m, window=0, sinks=0, scale=None, prefix=None):
     lse = torch.full((T, hq), -math.inf, dtype=torch.float64, device="cuda")
     e_u = torch.zeros(T, hq, dtype=torch.float64, device="cuda")
     cu, lens, P = m["cu_q"].tolist(), m["kv_lens"].tolist(), m["prefix"]
+    wide = d <= 128 and max(m["max_q"], T if P else 0) * (hq // hk) >= 64
     for b, n in enumerate(lens):
         nq = cu[b + 1] - cu[b]
         if not nq:
@@ -251,7 +256,10 @@ def reference(m, window=0, sinks=0, scale=None, prefix=None):
                 out[cu[b]:cu[b + 1], x], A[cu[b]:cu[b + 1], x] = w @ v, w @ v.abs()
                 lse[cu[b]:cu[b + 1], x] = l
                 s_max = torch.nan_to_num(k.abs().amax() / 7) if n else 0
-                e_u[cu[b]:cu[b + 1], x] = (d / 16 + 1) * 2.0 ** -22 * 80 * q[cu[b]:cu[b + 1], x].abs().sum(-1) * s_max * scale
+                e_u[cu[b]:cu[b + 1], x] = q[cu[b]:cu[b + 1], x].abs().sum(-1) * s_max * scale * (
+                    (d / 16 + 1) * 2.0 ** -22 * 80 + (7 * 2.0 ** -12 if wide else 0))
+                if wide and n:
+                    A[cu[b]:cu[b + 1], x] = 2 * A[cu[b]:cu[b + 1], x] + 2.0 ** -13 * torch.nan_to_num(v.abs().amax())
     return out, lse, A, e_u
 
 

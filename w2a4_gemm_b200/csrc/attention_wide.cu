@@ -5,21 +5,26 @@
 // Inference" names KV4.  The formula is attention.cu's.  A block takes two tiles of 128 rows against
 // the same keys, 128 at a time:
 //   S = Q K^T   (binary16 x binary16 -> fp32 in tensor memory)
-//   p_j = 2^(scale s_j S_j - ref) t_j, rounded to binary16 into tensor memory over S
+//   p_j = 2^(k S_j + e - ref), rounded to binary16 into tensor memory over S
 //   O += P V    (P from tensor memory, O stays there)
 // K and V come from the paged 4-bit cache: four warps read the codes into registers (a step ahead) and
-// write them as exact whole numbers in binary16 in the layout the tensor core reads: K rows of keys,
-// V transposed (rows of values, so that both operands are contiguous along the sum), 128-byte swizzled.
-// The scales stay apart in fp32, so no rounding is added.  The order of values inside each group of
-// eight is that in which a word's nibbles come out; Q is laid out alike.
+// write the values in binary16 in the layout the tensor core reads: K rows of keys, V transposed (rows
+// of values, so that both operands are contiguous along the sum), 128-byte swizzled.  The order of
+// values inside each group of eight is that in which a word's nibbles come out; Q is laid out alike.
+// A value is code * m / 2^e, m = 7 s the row's largest magnitude (a binary16 value, so the product is
+// the only rounding: 2^-12 of the value, that of the binary16 values qift_gather_kv returns) and 2^e the
+// power of two of the largest m of 32 keys; 2^e of K (with 1/7 and the softmax scale) is the factor k, that
+// of V the e above, so small values lose nothing.  With the exact codes as operands and the scales
+// applied to S and P, each row's thread reads 128 pairs of scales a step from shared memory: that read
+// took two thirds of the load pipe, and the prompt of 8192 tokens 951 us.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
 //   warps 8-11       unpack K, V; copy the scales
 //   warp 12          tensor-memory owner and issuer of the products (13-15 fill its register group)
 // Tile 1's products run while tile 0's softmax does, and the other way round.
 //
-// A row's reference is raised (and O scaled down) only when the weights of a step would not fit
-// binary16: the test is the step's sum of 2^u times its largest t_j, so it costs one product a row.
+// A row's reference is raised (and O scaled down) only when the weights of a step might not fit
+// binary16: the test is their sum, which is needed anyway.
 //
 // Every wait is bounded: one that runs out sets a shared abort flag and the device error word, every
 // role leaves its loop, the products in flight are waited for and tensor memory is freed.
@@ -43,7 +48,7 @@ constexpr int kUnpackThreads = 32 * kUnpackWarps;
 // Four groups of four warps, launched with 128 registers a thread and redistributed: a softmax thread holds a
 // row's 128 weights in pairs.  The shares sum to the four groups' 4 x 128.
 constexpr int kThreads = 32 * (kSoftWarps + kUnpackWarps + 4);
-constexpr int kSoftRegs = 176, kUnpackRegs = 104, kIssueRegs = 56;
+constexpr int kSoftRegs = 152, kUnpackRegs = 120, kIssueRegs = 88;
 static_assert(TILES == 2 && 2 * kSoftRegs + kUnpackRegs + kIssueRegs == 4 * 128, "registers of the launch");
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -69,8 +74,9 @@ struct Shape {
     static constexpr int VB = D == 64 ? 4 : 8;           // bytes of a value row that a thread transposes
     static constexpr int Q_BYTES = BM * D * 2, K_BYTES = BN * D * 2, V_BYTES = BN * D * 2;
     static constexpr int K_AT = TILES * Q_BYTES, V_AT = K_AT + STAGES * K_BYTES, SC_AT = V_AT + STAGES * V_BYTES;
-    static constexpr int BAR_AT = SC_AT + RING * (BN * 8 + 32);
-    static constexpr int SMEM = BAR_AT + 256 + 1024;
+    static constexpr int BAR_AT = SC_AT + RING * (BN * 2 + 36) + 16;
+    static constexpr int SMEM = BAR_AT + 256;
+    static_assert(BAR_AT % 16 == 0, "alignment");
     static constexpr int OPAD = D + 4;
     static_assert(TILES * BM * OPAD * 4 <= BAR_AT, "finished rows lie over the operands");
     static_assert(SMEM <= 232448, "shared memory");
@@ -101,21 +107,34 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort,
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// An operand's descriptor is given as its lower word (the address part); the upper is the same for all.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // as tc::smem_desc_sw128
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, {%6, %6, %6, %6}, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(0u)
         : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, {%6, %6, %6, %6}, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(0u)
         : "memory");
+}
+
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
 
 // Two fp32 at once.
@@ -147,6 +166,31 @@ __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint
 }
 __device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
 
+// Waits for this thread's loads from tensor memory; the values pass through, so that nothing that uses
+// them can be moved before the wait.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]),
+                   "+r"(x[16]), "+r"(x[17]), "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]),
+                   "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                   "+r"(x[30]), "+r"(x[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t mulh2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The largest magnitude of a row of the cache from its scale s = m / 7: 7 s rounds to m, a binary16
+// value.  What no row can have (a scale that was never written) counts as 0.
+__device__ __forceinline__ float scale7(float s) {
+    return s >= 0.0f && s <= 9358.0f ? __half2float(__float2half_rn(7.0f * s)) : 0.0f;
+}
+__device__ __forceinline__ int exponent(float m) { return max((int)(__float_as_uint(m) >> 23) - 127, -28); }
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // What a softmax thread knows of its row's view of a step, where not every row sees every key.
 struct View {
     int hi, lo, sinks;   // key j counts if j <= hi and (j > lo or j < sinks)
@@ -158,55 +202,57 @@ struct View {
     }
 };
 
-// Weights of one step: S of this thread's row from tensor memory, p (binary16 pairs) and the sum of 2^u.
+// Weights of one step: S of this thread's row from tensor memory, p = 2^(k S + e - ref) in binary16
+// pairs, k and e by chunk of 32 keys.  total: sum of p; the result: sum of 2^(k S - ref).
 template <bool MASK>
-__device__ __forceinline__ float weigh(uint32_t taddr, const float4* __restrict__ sc, float ref, const View& view,
-                                       uint32_t (&p)[BN / 2]) {
-    uint64_t sum = pack2(0.0f, 0.0f);
-    const uint64_t neg = pack2(-ref, -ref);
+__device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[4], const float (&e)[4], float ref,
+                                       const View& view, uint32_t (&p)[BN / 2], float& total) {
+    uint32_t in[2][32];
+    tc::tmem_ld_32x32b_x32(taddr, in[0]);
+    float part = 0.0f;
+    total = 0.0f;
+#pragma unroll
+    for (int c = 0; c < BN / 32; ++c) {
+        uint32_t(&x)[32] = in[c & 1];
+        tmem_ld_wait_for(x);
+        if (c + 1 < BN / 32) tc::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), in[(c + 1) & 1]);
+        const uint64_t k2 = pack2(k[c], k[c]), off = pack2(e[c] - ref, e[c] - ref);
+        uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float u0, u1;
+            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), k2, off), u0, u1);
+            if (MASK) {
+                u0 = view.sees(c * 32 + 2 * i) ? u0 : -INFINITY;
+                u1 = view.sees(c * 32 + 2 * i + 1) ? u1 : -INFINITY;
+            }
+            const float w0 = ex2(u0), w1 = ex2(u1);
+            sum = add2(sum, pack2(w0, w1));
+            const __half2 h = __floats2half2_rn(w0, w1);
+            p[c * 16 + i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        float s0, s1;
+        unpack2(sum, s0, s1);
+        s0 += s1;
+        total += s0;
+        part = __fmaf_rn(s0, ex2(-e[c]), part);
+    }
+    return part;
+}
+
+// The largest k S + e of a step.
+__device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[4], const float (&e)[4], const View& view,
+                                         bool mask) {
+    float top = -INFINITY;
 #pragma unroll
     for (int c = 0; c < BN / 32; ++c) {
         uint32_t x[32];
         tc::tmem_ld_32x32b_x32(taddr + 32 * c, x);
-        tc::tmem_ld_wait();
+        tmem_ld_wait_for(x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float4 f = sc[c * 16 + e];
-            float u0, u1, p0, p1;
-            unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), pack2(f.x, f.y), neg), u0, u1);
-            bool s0 = true, s1 = true;
-            if (MASK) {
-                s0 = view.sees(c * 32 + 2 * e), s1 = view.sees(c * 32 + 2 * e + 1);
-                u0 = s0 ? u0 : -INFINITY, u1 = s1 ? u1 : -INFINITY;
-            }
-            const uint64_t w = pack2(ex2(u0), ex2(u1));
-            sum = add2(sum, w);
-            unpack2(mul2(w, pack2(f.z, f.w)), p0, p1);
-            if (MASK) p0 = s0 ? p0 : 0.0f, p1 = s1 ? p1 : 0.0f;
-            const __half2 h = __floats2half2_rn(p0, p1);
-            p[c * 16 + e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
-    float s0, s1;
-    unpack2(sum, s0, s1);
-    return s0 + s1;
-}
-
-// The largest u_j + log2 t_j of a step.
-__device__ __forceinline__ float largest(uint32_t taddr, const float4* sc, const View& view, bool mask) {
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < BN / 16; ++c) {
-        uint32_t x[16];
-        tc::tmem_ld_32x32b_x16(taddr + 16 * c, x);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 f = sc[c * 8 + e];
-            const float u0 = __fmaf_rn(__uint_as_float(x[2 * e]), f.x, fmaxf(lg2(f.z), -28.0f));  // scales are 2^-24 / 7 or more
-            const float u1 = __fmaf_rn(__uint_as_float(x[2 * e + 1]), f.y, fmaxf(lg2(f.w), -28.0f));
-            if (!mask || view.sees(c * 16 + 2 * e)) top = fmaxf(top, u0);
-            if (!mask || view.sees(c * 16 + 2 * e + 1)) top = fmaxf(top, u1);
+        for (int i = 0; i < 32; ++i) {
+            const float u = __fmaf_rn(__uint_as_float(x[i]), k[c], e[c]);
+            if (!mask || view.sees(c * 32 + i)) top = fmaxf(top, u);
         }
     }
     return top;
@@ -216,13 +262,15 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_kernel(const AttentionArgs a, const Deal deal, long long limit, int stall) {
     using S = Shape<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];  // swizzled operands
     Bars& bar = *reinterpret_cast<Bars*>(smem + S::BAR_AT);
-    float4* scales = reinterpret_cast<float4*>(smem + S::SC_AT);                 // [RING][BN / 2]: two keys' s, two keys' t
-    float* v_most = reinterpret_cast<float*>(smem + S::SC_AT + RING * BN * 8);   // [RING][4]
-    uint32_t* gone = reinterpret_cast<uint32_t*>(v_most + RING * 4);             // [RING]
+    const uint32_t base32 = tc::smem_u32(smem);
+    float4* factor_k = reinterpret_cast<float4*>(smem + S::SC_AT);      // [RING] k of the step's four 32s of keys
+    float4* power_v = factor_k + RING;                                   // [RING] e
+    uint32_t* gone = reinterpret_cast<uint32_t*>(power_v + RING);        // [RING] 16s of keys that are not there
+    __half* ratio_v = reinterpret_cast<__half*>(gone + RING);            // [RING][BN]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in all lanes
     const int G = a.q_heads / a.kv_heads;
 
     // ---- which rows and keys
@@ -293,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (pos >= 0) atomicMin(&bar.pmin[tile], pos), atomicMax(&bar.pmax[tile], pos);
         }
         const __half* src = a.q + (token >= 0 ? token * a.q_stride + (int64_t)head * D : 0);
-        const uint32_t dst = tc::smem_u32(smem) + tile * S::Q_BYTES + r * 128;
+        const uint32_t dst = base32 + tile * S::Q_BYTES + r * 128;
 #pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -334,17 +382,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::tc_fence_after();
-            const float4* sc = scales + ring * (BN / 2);
-            const float4 m4 = reinterpret_cast<const float4*>(v_most)[ring];
-            const float most = kMostWeight / fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), 0x1p-28f);
+            const float4 k4 = factor_k[ring], e4 = power_v[ring];
+            const float k[4] = {k4.x, k4.y, k4.z, k4.w}, e[4] = {e4.x, e4.y, e4.z, e4.w};
             view.j0 = base + block_of(i) * BN;
             view.gone = gone[ring];
             const bool mask = !(view.j0 + BN - 1 <= t_least && view.j0 + BN <= base + range.limit && view.gone == 0 &&
                                 (!a.window || view.j0 > t_pmax - a.window || view.j0 + BN <= a.sinks));
             uint32_t p[BN / 2];
-            float part = mask ? weigh<true>(t_s, sc, ref, view, p) : weigh<false>(t_s, sc, ref, view, p);
-            if (!__all_sync(0xffffffffu, part <= most)) {  // also where it is no number
-                const float to = fmaxf(ref, largest(t_s, sc, view, mask) - kLift);
+            float total;
+            float part = mask ? weigh<true>(t_s, k, e, ref, view, p, total) : weigh<false>(t_s, k, e, ref, view, p, total);
+            if (!__all_sync(0xffffffffu, total <= kMostWeight)) {
+                const float to = fmaxf(ref, largest(t_s, k, e, view, mask) - kLift);
                 const float down = ex2(ref - to);
                 ref = to;
                 sum *= down;
@@ -358,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_ld_32x32b_x16(t_o + 16 * c, x);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * down);
+                        for (int q = 0; q < 16; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * down);
                         asm volatile(
                             "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
                             "%14,%15,%16};" ::"r"(t_o + 16 * c),
@@ -368,15 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::tmem_st_wait();
                 }
-                part = mask ? weigh<true>(t_s, sc, ref, view, p) : weigh<false>(t_s, sc, ref, view, p);
+                part = mask ? weigh<true>(t_s, k, e, ref, view, p, total) : weigh<false>(t_s, k, e, ref, view, p, total);
             }
             sum += part;
             uint32_t half[32];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) half[e] = p[32 * k + e];
-                tc::tmem_st_32x32b_x32(t_s + 32 * k, half);
+                for (int c = 0; c < 32; ++c) half[c] = p[32 * q + c];
+                tc::tmem_st_32x32b_x32(t_s + 32 * q, half);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
@@ -414,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tk < 0) continue;
                 float acc[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = rows[k * S::OPAD + lane * E + e];
+                for (int e = 0; e < E; ++e) acc[e] = rows[k * S::OPAD + lane * E + e] * (1.0f / 7.0f);
                 if (deal.slots == 0) {
                     finish_row<D>(a, acc, M, L, tk, hd, lane);
                 } else {
@@ -462,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t place = __shfl_sync(0xffffffffu, places, u >> 4);
             ks = vs = 0.0f;
             if (place != kNowhere && block_of(i) * BN + u < range.limit) {
-                ks = __ldg(a.k_scales + (uint64_t)place * 16 + (u & 15)) * a.scale_log2;
+                ks = __ldg(a.k_scales + (uint64_t)place * 16 + (u & 15));
                 vs = __ldg(a.v_scales + (uint64_t)place * 16 + (u & 15));
             }
         };
@@ -487,28 +535,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= STAGES &&
                 !__all_sync(0xffffffffu, wait(&bar.k_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
                 break;
-            // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free
-            float* sc = reinterpret_cast<float*>(scales + ring * (BN / 2) + (u >> 1)) + (u & 1);
-            sc[0] = ks;
-            sc[2] = vs;
-            float top = vs;
+            // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free.
+            // This warp's 32 keys are a chunk: m = 7 s by a power of two, that of the largest.
+            const float mk = scale7(ks), mv = scale7(vs);
+            float most_k = mk, most_v = mv;
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-            if (lane == 0) v_most[ring * 4 + w] = top;
+            for (int m = 16; m > 0; m >>= 1) {
+                most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, m));
+                most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, m));
+            }
+            const int ek = exponent(most_k), ev = exponent(most_v);
+            const uint32_t rk = __half_as_ushort(__float2half_rn(mk * power(-ek)));
+            ratio_v[ring * BN + u] = __float2half_rn(mv * power(-ev));
             const uint32_t away = __ballot_sync(0xffffffffu, lane < 8 && now == kNowhere);
-            if (u == 0) gone[ring] = away;
+            if (lane == 0) {
+                reinterpret_cast<float*>(factor_k + ring)[w] = power(ek) * (a.scale_log2 * (1.0f / 7.0f));
+                reinterpret_cast<float*>(power_v + ring)[w] = (float)ev;
+                if (w == 0) gone[ring] = away;
+            }
             tc::mbar_arrive(&bar.scales[ring]);
-            const uint32_t k_to = tc::smem_u32(smem + S::K_AT + st * S::K_BYTES);
+            const uint32_t k_to = base32 + S::K_AT + st * S::K_BYTES;
 #pragma unroll
             for (int q = 0; q < S::CH; ++q) {
                 const int v = (w * S::CH + q) * 4 + l4, kg = v / S::CH, cc = v % S::CH;
                 const uint32_t words[4] = {kq[q].x, kq[q].y, kq[q].z, kq[q].w};
+                const uint32_t r1 = __shfl_sync(0xffffffffu, rk, kg * 8 + l8 - 32 * w), r2 = r1 | (r1 << 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = cc * 4 + e;  // which group of eight values
                     const uint32_t x = words[e], y = words[e] >> 8;
-                    sts128(k_to + (c >> 3) * (BN * 128) + (kg * 8 + l8) * 128 + (((c & 7) ^ l8) << 4), nib.lo(x), nib.hi(x),
-                           nib.lo(y), nib.hi(y));
+                    sts128(k_to + (c >> 3) * (BN * 128) + (kg * 8 + l8) * 128 + (((c & 7) ^ l8) << 4),
+                           mulh2(nib.lo(x), r2), mulh2(nib.hi(x), r2), mulh2(nib.lo(y), r2), mulh2(nib.hi(y), r2));
                 }
             }
             if (i + 1 < n) load_k(next, i + 1);
@@ -517,7 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= STAGES &&
                 !__all_sync(0xffffffffu, wait(&bar.v_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
                 break;
-            const uint32_t v_to = tc::smem_u32(smem + S::V_AT + st * S::V_BYTES) + (v_kg >> 3) * (D * 128);
+            asm volatile("bar.sync 2, %0;" ::"n"(kUnpackThreads) : "memory");  // all four warps' ratios
+            const uint4 rv4 = *reinterpret_cast<const uint4*>(ratio_v + ring * BN + v_kg * 8);
+            const uint32_t rv[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
+            const uint32_t v_to = base32 + S::V_AT + st * S::V_BYTES + (v_kg >> 3) * (D * 128);
 #pragma unroll
             for (int wd = 0; wd < S::VB / 4; ++wd)
 #pragma unroll
@@ -531,9 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 2; ++e) {
                         const int d8 = 4 * hf + 2 * e;  // value's place among the word's eight
                         const uint32_t to = v_to + (v_dc * (2 * S::VB) + wd * 8 + d8) * 128;
-                        sts128(to + (((v_kg & 7) ^ d8) << 4), nib.lo(x[0]), nib.lo(x[1]), nib.lo(x[2]), nib.lo(x[3]));
-                        sts128(to + 128 + (((v_kg & 7) ^ (d8 + 1)) << 4), nib.hi(x[0]), nib.hi(x[1]), nib.hi(x[2]),
-                               nib.hi(x[3]));
+                        sts128(to + (((v_kg & 7) ^ d8) << 4), mulh2(nib.lo(x[0]), rv[0]), mulh2(nib.lo(x[1]), rv[1]),
+                               mulh2(nib.lo(x[2]), rv[2]), mulh2(nib.lo(x[3]), rv[3]));
+                        sts128(to + 128 + (((v_kg & 7) ^ (d8 + 1)) << 4), mulh2(nib.hi(x[0]), rv[0]),
+                               mulh2(nib.hi(x[1]), rv[1]), mulh2(nib.hi(x[2]), rv[2]), mulh2(nib.hi(x[3]), rv[3]));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[k] >>= 8;
                     }
@@ -549,57 +610,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ----------------------------------------------------------------------------- products
         // S of a step follows only when the tile's P V before it is complete, since P lies over S; the
         // other tile's products fill the time.
+// The whole warp runs the loop and one lane, always the same, issues: what the issue needs is then
+        // the same in all lanes and lies in the uniform registers that it is read from.  With the loop in
+        // one lane, each operand is moved there first, and eight products took 570 cycles to issue.
         constexpr uint32_t id_s = idesc_f16(BM, BN), id_o = idesc_f16(BM, D);
-        const uint64_t q0 = tc::smem_desc_sw128(tc::smem_u32(smem));
-        const uint64_t k0 = tc::smem_desc_sw128(tc::smem_u32(smem + S::K_AT));
-        const uint64_t v0 = tc::smem_desc_sw128(tc::smem_u32(smem + S::V_AT));
-        const bool issuer = warp == kSoftWarps + kUnpackWarps && lane == 0;
+        const bool issuer = warp_u == kSoftWarps + kUnpackWarps;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), b32 = __shfl_sync(0xffffffffu, base32, 0);
+        const int steps = __shfl_sync(0xffffffffu, n, 0);
+        const uint32_t q0 = desc_low(b32), k0 = desc_low(b32 + S::K_AT), v0 = desc_low(b32 + S::V_AT);
+        const bool one = elect();
         auto product_s = [&](int t, int st) {
+            const uint32_t q = q0 + t * (S::Q_BYTES >> 4), k1 = k0 + st * (S::K_BYTES >> 4);
+            if (one) {
 #pragma unroll
-            for (int c = 0; c < S::CB; ++c)
+                for (int c = 0; c < S::CB; ++c)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ss(tmem + t * BN, q0 + (uint64_t)((t * S::Q_BYTES + c * BM * 128) >> 4) + 2 * k,
-                               k0 + (uint64_t)((st * S::K_BYTES + c * BN * 128) >> 4) + 2 * k, id_s, c + k != 0);
-            tc::mma_commit(&bar.s_full[t]);
-        };
-        bool ok = issuer;
-        if (stall && issuer) ok = wait(&bar.never, 0, &bar.abort, limit);  // test hook
-        if (n > 0 && issuer) {
-            ok = ok && wait(&bar.k_full[0], 0, &bar.abort, limit);
-            if (ok) {
-                tc::tc_fence_after();
-                for (int t = 0; t < TILES; ++t) product_s(t, 0);
-                tc::mma_commit(&bar.k_empty[0]);
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_ss(tm + t * BN, q + ((c * BM * 128) >> 4) + 2 * k, k1 + ((c * BN * 128) >> 4) + 2 * k, id_s,
+                                   c + k != 0);
+                tc::mma_commit(&bar.s_full[t]);
             }
-        }
-        for (int i = 0; ok && i < n; ++i) {
-            const int st = i % STAGES, sn = (i + 1) % STAGES;
-            ok = wait(&bar.v_full[st], (i / STAGES) & 1, &bar.abort, limit);
-            for (int t = 0; ok && t < TILES; ++t) {
-                ok = wait(&bar.p_full[t], i & 1, &bar.abort, limit);
-                if (!ok) break;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    mma_f16_ts(tmem + 2 * BN + t * D, tmem + t * BN + k * 8,
-                               v0 + (uint64_t)((st * S::V_BYTES + (k >> 2) * D * 128) >> 4) + 2 * (k & 3), id_o,
-                               (i | k) != 0);
-                tc::mma_commit(&bar.o_done[t]);
-                if (t == TILES - 1) tc::mma_commit(&bar.v_empty[st]);
-                if (i + 1 < n) {
-                    ok = (t > 0 || wait(&bar.k_full[sn], ((i + 1) / STAGES) & 1, &bar.abort, limit)) &&
-                         wait(&bar.o_done[t], i & 1, &bar.abort, limit);
-                    if (!ok) break;
+        };
+        auto commit = [&](uint64_t* to) {
+            if (one) tc::mma_commit(to);
+        };
+        auto wait_all = [&](uint64_t* on, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait(on, parity, &bar.abort, limit));
+        };
+        if (issuer) {
+            bool ok = true;
+            if (stall) ok = wait_all(&bar.never, 0);  // test hook
+            if (steps > 0) {
+                ok = ok && wait_all(&bar.k_full[0], 0);
+                if (ok) {
                     tc::tc_fence_after();
-                    product_s(t, sn);
-                    if (t == TILES - 1) tc::mma_commit(&bar.k_empty[sn]);
+                    for (int t = 0; t < TILES; ++t) product_s(t, 0);
+                    commit(&bar.k_empty[0]);
                 }
             }
-        }
-        // Nothing may still read this block's memory when it leaves, also after an abort.
-        if (issuer) {
-            tc::mma_commit(&bar.done);
+            for (int i = 0; ok && i < steps; ++i) {
+                const int st = i % STAGES, sn = (i + 1) % STAGES;
+                ok = wait_all(&bar.v_full[st], (i / STAGES) & 1);
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    ok = ok && wait_all(&bar.p_full[t], i & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint32_t v1 = v0 + st * (S::V_BYTES >> 4);
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < BN / 16; ++k)
+                            mma_f16_ts(tm + 2 * BN + t * D, tm + t * BN + k * 8,
+                                       v1 + (((k >> 2) * D * 128) >> 4) + 2 * (k & 3), id_o, k != 0 ? 1u : (uint32_t)i);
+                        tc::mma_commit(&bar.o_done[t]);
+                    }
+                    if (t == TILES - 1) commit(&bar.v_empty[st]);
+                    if (i + 1 < steps) {
+                        ok = (t > 0 || wait_all(&bar.k_full[sn], ((i + 1) / STAGES) & 1)) &&
+                             wait_all(&bar.o_done[t], i & 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        product_s(t, sn);
+                        if (t == TILES - 1) commit(&bar.k_empty[sn]);
+                    }
+                }
+            }
+            // Nothing may still read this block's memory when it leaves, also after an abort.
+            commit(&bar.done);
             int zero = 0;
             tc::mbar_wait_bounded(&bar.done, 0, &zero, limit);
         }
