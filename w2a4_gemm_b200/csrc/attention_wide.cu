@@ -41,7 +41,7 @@ namespace wide {
 
 __device__ int g_error = 0;  // bit 1: a wait ran out (read by qift_device_error)
 
-constexpr int BM = 128, BN = kWideStep, TILES = 2, STAGES = 2, RING = 4;
+constexpr int BM = 128, BN = kWideStep, BH = BN / 2, TILES = 2, STAGES = 2, RING = 4;
 static_assert(BM * TILES == kWideRows, "rows of a block");
 constexpr int kSoftWarps = 4 * TILES, kUnpackWarps = 4;
 constexpr int kUnpackThreads = 32 * kUnpackWarps;
@@ -86,7 +86,7 @@ struct Shape {
 struct Bars {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t scales[RING];
-    uint64_t s_full[TILES], p_full[TILES], o_done[TILES];
+    uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES];
     uint64_t done, never;
     uint32_t tmem;
     int abort;
@@ -115,8 +115,8 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, u
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
         "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, {%6, %6, %6, %6}, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(0u)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
         : "memory");
 }
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
@@ -124,8 +124,8 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, u
         "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
         "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, {%6, %6, %6, %6}, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(0u)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
         : "memory");
 }
 
@@ -191,6 +191,15 @@ __device__ __forceinline__ float scale7(float s) {
 __device__ __forceinline__ int exponent(float m) { return max((int)(__float_as_uint(m) >> 23) - 127, -28); }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
+        "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+        : "memory");
+}
+
 // What a softmax thread knows of its row's view of a step, where not every row sees every key.
 struct View {
     int hi, lo, sinks;   // key j counts if j <= hi and (j > lo or j < sinks)
@@ -202,20 +211,21 @@ struct View {
     }
 };
 
-// Weights of one step: S of this thread's row from tensor memory, p = 2^(k S + e - ref) in binary16
-// pairs, k and e by chunk of 32 keys.  total: sum of p; the result: sum of 2^(k S - ref).
+// Weights of half a step: S of this thread's row from tensor memory, p = 2^(k S + e - ref) in binary16
+// pairs, k and e by chunk of 32 keys; `first` is the half's first key in the view.  total: sum of p; the
+// result: sum of 2^(k S - ref).
 template <bool MASK>
-__device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[4], const float (&e)[4], float ref,
-                                       const View& view, uint32_t (&p)[BN / 2], float& total) {
+__device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[2], const float (&e)[2], float ref,
+                                       const View& view, int first, uint32_t (&p)[BH / 2], float& total) {
     uint32_t in[2][32];
     tc::tmem_ld_32x32b_x32(taddr, in[0]);
     float part = 0.0f;
     total = 0.0f;
 #pragma unroll
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = 0; c < BH / 32; ++c) {
         uint32_t(&x)[32] = in[c & 1];
         tmem_ld_wait_for(x);
-        if (c + 1 < BN / 32) tc::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), in[(c + 1) & 1]);
+        if (c + 1 < BH / 32) tc::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), in[(c + 1) & 1]);
         const uint64_t k2 = pack2(k[c], k[c]), off = pack2(e[c] - ref, e[c] - ref);
         uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
@@ -223,8 +233,8 @@ __device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[4], cons
             float u0, u1;
             unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), k2, off), u0, u1);
             if (MASK) {
-                u0 = view.sees(c * 32 + 2 * i) ? u0 : -INFINITY;
-                u1 = view.sees(c * 32 + 2 * i + 1) ? u1 : -INFINITY;
+                u0 = view.sees(first + c * 32 + 2 * i) ? u0 : -INFINITY;
+                u1 = view.sees(first + c * 32 + 2 * i + 1) ? u1 : -INFINITY;
             }
             const float w0 = ex2(u0), w1 = ex2(u1);
             sum = add2(sum, pack2(w0, w1));
@@ -240,19 +250,19 @@ __device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[4], cons
     return part;
 }
 
-// The largest k S + e of a step.
-__device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[4], const float (&e)[4], const View& view,
-                                         bool mask) {
+// The largest k S + e of half a step.
+__device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[2], const float (&e)[2], const View& view,
+                                         int first, bool mask) {
     float top = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < BN / 32; ++c) {
+    for (int c = 0; c < BH / 32; ++c) {
         uint32_t x[32];
         tc::tmem_ld_32x32b_x32(taddr + 32 * c, x);
         tmem_ld_wait_for(x);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const float u = __fmaf_rn(__uint_as_float(x[i]), k[c], e[c]);
-            if (!mask || view.sees(c * 32 + i)) top = fmaxf(top, u);
+            if (!mask || view.sees(first + c * 32 + i)) top = fmaxf(top, u);
         }
     }
     return top;
@@ -299,8 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < RING; ++i) tc::mbar_init(&bar.scales[i], kUnpackThreads);
         for (int i = 0; i < TILES; ++i) {
-            tc::mbar_init(&bar.s_full[i], 1);
-            tc::mbar_init(&bar.p_full[i], BM);
+            for (int half = 0; half < 2; ++half) {
+                tc::mbar_init(&bar.s_full[i][half], 1);
+                tc::mbar_init(&bar.p_full[i][half], BM);
+            }
             tc::mbar_init(&bar.o_done[i], 1);
             bar.pmin[i] = bar.least[i] = 0x7fffffff;
             bar.pmax[i] = -1;
@@ -375,62 +387,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         view.lo = a.window ? pos - a.window : -1;
         view.sinks = a.sinks;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; ok && i < n; ++i) {
             const int ring = i % RING;
-            ok = wait(&bar.scales[ring], (i / RING) & 1, &bar.abort, limit) &&
-                 wait(&bar.s_full[tile], i & 1, &bar.abort, limit);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = __all_sync(0xffffffffu, wait(&bar.scales[ring], (i / RING) & 1, &bar.abort, limit));
             if (!ok) break;
-            tc::tc_fence_after();
             const float4 k4 = factor_k[ring], e4 = power_v[ring];
-            const float k[4] = {k4.x, k4.y, k4.z, k4.w}, e[4] = {e4.x, e4.y, e4.z, e4.w};
             view.j0 = base + block_of(i) * BN;
             view.gone = gone[ring];
             const bool mask = !(view.j0 + BN - 1 <= t_least && view.j0 + BN <= base + range.limit && view.gone == 0 &&
                                 (!a.window || view.j0 > t_pmax - a.window || view.j0 + BN <= a.sinks));
-            uint32_t p[BN / 2];
-            float total;
-            float part = mask ? weigh<true>(t_s, k, e, ref, view, p, total) : weigh<false>(t_s, k, e, ref, view, p, total);
-            if (!__all_sync(0xffffffffu, total <= kMostWeight)) {
-                const float to = fmaxf(ref, largest(t_s, k, e, view, mask) - kLift);
-                const float down = ex2(ref - to);
-                ref = to;
-                sum *= down;
-                if (i > 0) {
-                    ok = __all_sync(0xffffffffu, wait(&bar.o_done[tile], (i - 1) & 1, &bar.abort, limit));
-                    if (!ok) break;
-                    tc::tc_fence_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float k[2] = {half ? k4.z : k4.x, half ? k4.w : k4.y};
+                const float e[2] = {half ? e4.z : e4.x, half ? e4.w : e4.y};
+                const uint32_t t_h = t_s + half * BH;
+                ok = __all_sync(0xffffffffu, wait(&bar.s_full[tile][half], i & 1, &bar.abort, limit));
+                if (!ok) break;
+                tc::tc_fence_after();
+                uint32_t p[BH / 2];
+                float total;
+                float part = mask ? weigh<true>(t_h, k, e, ref, view, half * BH, p, total)
+                                  : weigh<false>(t_h, k, e, ref, view, half * BH, p, total);
+                if (!__all_sync(0xffffffffu, total <= kMostWeight)) {
+                    const float to = fmaxf(ref, largest(t_h, k, e, view, half * BH, mask) - kLift);
+                    const float down = ex2(ref - to);
+                    ref = to;
+                    sum *= down;
+                    if (i + half > 0) {  // the product of the half before
+                        ok = __all_sync(0xffffffffu, wait(&bar.o_done[tile], half ^ 1, &bar.abort, limit));
+                        if (!ok) break;
+                        tc::tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t x[16];
-                        tc::tmem_ld_32x32b_x16(t_o + 16 * c, x);
-                        tc::tmem_ld_wait();
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t x[16];
+                            tc::tmem_ld_32x32b_x16(t_o + 16 * c, x);
+                            tc::tmem_ld_wait();
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * down);
-                        asm volatile(
-                            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-                            "%14,%15,%16};" ::"r"(t_o + 16 * c),
-                            "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]),
-                            "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
-                            : "memory");
+                            for (int q = 0; q < 16; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * down);
+                            tmem_st_x16(t_o + 16 * c, x);
+                        }
+                        tc::tmem_st_wait();
                     }
-                    tc::tmem_st_wait();
+                    part = mask ? weigh<true>(t_h, k, e, ref, view, half * BH, p, total)
+                                : weigh<false>(t_h, k, e, ref, view, half * BH, p, total);
                 }
-                part = mask ? weigh<true>(t_s, k, e, ref, view, p, total) : weigh<false>(t_s, k, e, ref, view, p, total);
+                sum += part;
+                tc::tmem_st_32x32b_x32(t_h, p);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&bar.p_full[tile][half]);
             }
-            sum += part;
-            uint32_t half[32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) half[c] = p[32 * q + c];
-                tc::tmem_st_32x32b_x32(t_s + 32 * q, half);
-            }
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            tc::mbar_arrive(&bar.p_full[tile]);
         }
-        if (n > 0 && ok) ok = wait(&bar.o_done[tile], (n - 1) & 1, &bar.abort, limit);
+        if (n > 0 && ok) ok = wait(&bar.o_done[tile], 1, &bar.abort, limit);  // half-step 2 n - 1
         ok = __all_sync(0xffffffffu, ok);
         soft_bar();  // both tiles' products are done: the operands' memory is free
         // Rows through shared memory, so that a warp finishes one together (rotation back, whole lines).
@@ -608,71 +616,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         fewer_registers<kIssueRegs>();
         // ----------------------------------------------------------------------------- products
-        // S of a step follows only when the tile's P V before it is complete, since P lies over S; the
-        // other tile's products fill the time.
-// The whole warp runs the loop and one lane, always the same, issues: what the issue needs is then
+        // By half steps of 64 keys: a tile has two places for S, P lies over the S that it comes from, and S
+        // of half step j + 2 follows when P V of half step j is complete.  So the softmax of a half step has
+        // its S while the products of the half steps beside it run.  With one place of 128 keys it waited
+        // for P V and S in turn (750 us for the prompt of 8192 tokens).
+        // The whole warp runs the loop and one lane, always the same, issues: what the issue needs is then
         // the same in all lanes and lies in the uniform registers that it is read from.  With the loop in
         // one lane, each operand is moved there first, and eight products took 570 cycles to issue.
-        constexpr uint32_t id_s = idesc_f16(BM, BN), id_o = idesc_f16(BM, D);
+        constexpr uint32_t id_s = idesc_f16(BM, BH), id_o = idesc_f16(BM, D);
         const bool issuer = warp_u == kSoftWarps + kUnpackWarps;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), b32 = __shfl_sync(0xffffffffu, base32, 0);
-        const int steps = __shfl_sync(0xffffffffu, n, 0);
+        const int halves = 2 * __shfl_sync(0xffffffffu, n, 0);
         const uint32_t q0 = desc_low(b32), k0 = desc_low(b32 + S::K_AT), v0 = desc_low(b32 + S::V_AT);
         const bool one = elect();
-        auto product_s = [&](int t, int st) {
-            const uint32_t q = q0 + t * (S::Q_BYTES >> 4), k1 = k0 + st * (S::K_BYTES >> 4);
-            if (one) {
-#pragma unroll
-                for (int c = 0; c < S::CB; ++c)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ss(tm + t * BN, q + ((c * BM * 128) >> 4) + 2 * k, k1 + ((c * BN * 128) >> 4) + 2 * k, id_s,
-                                   c + k != 0);
-                tc::mma_commit(&bar.s_full[t]);
-            }
-        };
         auto commit = [&](uint64_t* to) {
             if (one) tc::mma_commit(to);
         };
         auto wait_all = [&](uint64_t* on, uint32_t parity) {
             return __all_sync(0xffffffffu, wait(on, parity, &bar.abort, limit));
         };
+        auto product_s = [&](int t, int j) {
+            const int half = j & 1, st = (j >> 1) % STAGES;
+            const uint32_t q = q0 + t * (S::Q_BYTES >> 4);
+            const uint32_t k1 = k0 + st * (S::K_BYTES >> 4) + half * ((BH * 128) >> 4);
+            const uint32_t to = tm + t * BN + half * BH;
+            if (one) {
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_ss(to, q + ((c * BM * 128) >> 4) + 2 * k, k1 + ((c * BN * 128) >> 4) + 2 * k, id_s,
+                                   c + k != 0);
+                tc::mma_commit(&bar.s_full[t][half]);
+                if (half == 1 && t == TILES - 1) tc::mma_commit(&bar.k_empty[st]);
+            }
+        };
+        auto product_o = [&](int t, int j) {
+            const int half = j & 1, st = (j >> 1) % STAGES;
+            const uint32_t v1 = v0 + st * (S::V_BYTES >> 4) + half * ((D * 128) >> 4);
+            const uint32_t p = tm + t * BN + half * BH, to = tm + 2 * BN + t * D;
+            if (one) {
+#pragma unroll
+                for (int k = 0; k < BH / 16; ++k)
+                    mma_f16_ts(to, p + k * 8, v1 + 2 * k, id_o, k != 0 ? 1u : (uint32_t)j);
+                tc::mma_commit(&bar.o_done[t]);
+                if (half == 1 && t == TILES - 1) tc::mma_commit(&bar.v_empty[st]);
+            }
+        };
         if (issuer) {
             bool ok = true;
             if (stall) ok = wait_all(&bar.never, 0);  // test hook
-            if (steps > 0) {
+            if (halves > 0) {
                 ok = ok && wait_all(&bar.k_full[0], 0);
                 if (ok) {
                     tc::tc_fence_after();
-                    for (int t = 0; t < TILES; ++t) product_s(t, 0);
-                    commit(&bar.k_empty[0]);
+                    for (int j = 0; j < 2; ++j)
+                        for (int t = 0; t < TILES; ++t) product_s(t, j);
                 }
             }
-            for (int i = 0; ok && i < steps; ++i) {
-                const int st = i % STAGES, sn = (i + 1) % STAGES;
-                ok = wait_all(&bar.v_full[st], (i / STAGES) & 1);
-#pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    ok = ok && wait_all(&bar.p_full[t], i & 1);
+            for (int j = 0; ok && j < halves; ++j) {
+                const int i = j >> 1, half = j & 1;
+                if (half == 0) ok = wait_all(&bar.v_full[i % STAGES], (i / STAGES) & 1);
+                for (int t = 0; ok && t < TILES; ++t) {
+                    ok = wait_all(&bar.p_full[t][half], i & 1);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint32_t v1 = v0 + st * (S::V_BYTES >> 4);
-                    if (one) {
-#pragma unroll
-                        for (int k = 0; k < BN / 16; ++k)
-                            mma_f16_ts(tm + 2 * BN + t * D, tm + t * BN + k * 8,
-                                       v1 + (((k >> 2) * D * 128) >> 4) + 2 * (k & 3), id_o, k != 0 ? 1u : (uint32_t)i);
-                        tc::mma_commit(&bar.o_done[t]);
-                    }
-                    if (t == TILES - 1) commit(&bar.v_empty[st]);
-                    if (i + 1 < steps) {
-                        ok = (t > 0 || wait_all(&bar.k_full[sn], ((i + 1) / STAGES) & 1)) &&
-                             wait_all(&bar.o_done[t], i & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        product_s(t, sn);
-                        if (t == TILES - 1) commit(&bar.k_empty[sn]);
-                    }
+                    product_o(t, j);
+                }
+                if (!ok || j + 2 >= halves) continue;
+                if (half == 0) ok = wait_all(&bar.k_full[(i + 1) % STAGES], ((i + 1) / STAGES) & 1);
+                for (int t = 0; ok && t < TILES; ++t) {
+                    ok = wait_all(&bar.o_done[t], half);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    product_s(t, j + 2);
                 }
             }
             // Nothing may still read this block's memory when it leaves, also after an abort.
