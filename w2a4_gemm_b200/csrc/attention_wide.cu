@@ -20,8 +20,8 @@
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
 //   warps 8-11       unpack K, V; copy the scales
-//   warp 12          tensor-memory owner and issuer of the products (13-15 fill its register group)
-// Tile 1's products run while tile 0's softmax does, and the other way round.
+//   warps 12, 13     issue the products of tile 0, 1 (12 owns tensor memory; 14 and 15 fill the register group)
+// One tile's products run under the other's softmax.
 //
 // A row's reference is raised (and O scaled down) only when the weights of a step might not fit
 // binary16: the test is their sum, which is needed anyway.
@@ -86,7 +86,7 @@ struct Shape {
 struct Bars {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t scales[RING];
-    uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES];
+    uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES][2];  // by halves of a step
     uint64_t done, never;
     uint32_t tmem;
     int abort;
@@ -303,21 +303,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             tc::mbar_init(&bar.k_full[i], kUnpackThreads);
-            tc::mbar_init(&bar.k_empty[i], 1);
+            tc::mbar_init(&bar.k_empty[i], TILES);
             tc::mbar_init(&bar.v_full[i], kUnpackThreads);
-            tc::mbar_init(&bar.v_empty[i], 1);
+            tc::mbar_init(&bar.v_empty[i], TILES);
         }
         for (int i = 0; i < RING; ++i) tc::mbar_init(&bar.scales[i], kUnpackThreads);
         for (int i = 0; i < TILES; ++i) {
             for (int half = 0; half < 2; ++half) {
                 tc::mbar_init(&bar.s_full[i][half], 1);
                 tc::mbar_init(&bar.p_full[i][half], BM);
+                tc::mbar_init(&bar.o_done[i][half], 1);
             }
-            tc::mbar_init(&bar.o_done[i], 1);
             bar.pmin[i] = bar.least[i] = 0x7fffffff;
             bar.pmax[i] = -1;
         }
-        tc::mbar_init(&bar.done, 1);
+        tc::mbar_init(&bar.done, TILES);
         tc::mbar_init(&bar.never, 1);
         bar.abort = 0;
         tc::fence_mbar_init();
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ref = to;
                     sum *= down;
                     if (i + half > 0) {  // the product of the half before
-                        ok = __all_sync(0xffffffffu, wait(&bar.o_done[tile], half ^ 1, &bar.abort, limit));
+                        ok = __all_sync(0xffffffffu, wait(&bar.o_done[tile][half ^ 1], (i - 1 + half) & 1, &bar.abort, limit));
                         if (!ok) break;
                         tc::tc_fence_after();
 #pragma unroll 1
@@ -432,13 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 : weigh<false>(t_h, k, e, ref, view, half * BH, p, total);
                 }
                 sum += part;
-                tc::tmem_st_32x32b_x32(t_h, p);
+                tc::tmem_st_32x32b_x32(t_h, p);  // over the S that is read
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&bar.p_full[tile][half]);
             }
         }
-        if (n > 0 && ok) ok = wait(&bar.o_done[tile], 1, &bar.abort, limit);  // half-step 2 n - 1
+        if (n > 0 && ok) ok = wait(&bar.o_done[tile][1], (n - 1) & 1, &bar.abort, limit);
         ok = __all_sync(0xffffffffu, ok);
         soft_bar();  // both tiles' products are done: the operands' memory is free
         // Rows through shared memory, so that a warp finishes one together (rotation back, whole lines).
@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                            mulh2(nib.lo(x), r2), mulh2(nib.hi(x), r2), mulh2(nib.lo(y), r2), mulh2(nib.hi(y), r2));
                 }
             }
-            if (i + 1 < n) load_k(next, i + 1);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&bar.k_full[st]);
+            if (i + 1 < n) load_k(next, i + 1);  // behind the fence, which would wait for the loads
             if (i >= STAGES &&
                 !__all_sync(0xffffffffu, wait(&bar.v_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
                 break;
@@ -607,9 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) x[k] >>= 8;
                     }
                 }
-            if (i + 1 < n) load_v(next);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&bar.v_full[st]);
+            if (i + 1 < n) load_v(next);
             now = next;
             next = find(i + 2);
         }
@@ -617,83 +617,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers<kIssueRegs>();
         // ----------------------------------------------------------------------------- products
         // By half steps of 64 keys: a tile has two places for S, P lies over the S that it comes from, and S
-        // of half step j + 2 follows when P V of half step j is complete.  So the softmax of a half step has
-        // its S while the products of the half steps beside it run.  With one place of 128 keys it waited
-        // for P V and S in turn (750 us for the prompt of 8192 tokens).
+        // of half step j + 2 follows when P V of half step j is complete; so a half step's softmax has its S
+        // while the products beside it run.  Each tile has a warp that issues its products (about 50 cycles
+        // each, whatever their size): one warp for both, in a fixed order, made the tiles fall into step and
+        // wait for each other (730 us for the prompt of 8192 tokens), and looking for the tile that can go
+        // on took longer still (791 us).
         // The whole warp runs the loop and one lane, always the same, issues: what the issue needs is then
-        // the same in all lanes and lies in the uniform registers that it is read from.  With the loop in
-        // one lane, each operand is moved there first, and eight products took 570 cycles to issue.
+        // the same in all lanes; with the loop in one lane an issue took 72 cycles.
         constexpr uint32_t id_s = idesc_f16(BM, BH), id_o = idesc_f16(BM, D);
-        const bool issuer = warp_u == kSoftWarps + kUnpackWarps;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), b32 = __shfl_sync(0xffffffffu, base32, 0);
-        const int halves = 2 * __shfl_sync(0xffffffffu, n, 0);
-        const uint32_t q0 = desc_low(b32), k0 = desc_low(b32 + S::K_AT), v0 = desc_low(b32 + S::V_AT);
-        const bool one = elect();
-        auto commit = [&](uint64_t* to) {
-            if (one) tc::mma_commit(to);
-        };
-        auto wait_all = [&](uint64_t* on, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait(on, parity, &bar.abort, limit));
-        };
-        auto product_s = [&](int t, int j) {
-            const int half = j & 1, st = (j >> 1) % STAGES;
-            const uint32_t q = q0 + t * (S::Q_BYTES >> 4);
-            const uint32_t k1 = k0 + st * (S::K_BYTES >> 4) + half * ((BH * 128) >> 4);
-            const uint32_t to = tm + t * BN + half * BH;
-            if (one) {
+        const int t = warp_u - (kSoftWarps + kUnpackWarps);  // this warp's tile
+        if (t < TILES) {
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), b32 = __shfl_sync(0xffffffffu, base32, 0);
+            const int halves = 2 * __shfl_sync(0xffffffffu, n, 0);
+            const uint32_t q0 = desc_low(b32 + t * S::Q_BYTES), k0 = desc_low(b32 + S::K_AT), v0 = desc_low(b32 + S::V_AT);
+            const uint32_t t_s = tm + t * BN, t_o = tm + 2 * BN + t * D;
+            const bool one = elect();
+            auto wait_all = [&](uint64_t* on, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait(on, parity, &bar.abort, limit));
+            };
+            auto product_s = [&](int j) {
+                const int half = j & 1, st = (j >> 1) % STAGES;
+                const uint32_t k1 = k0 + st * (S::K_BYTES >> 4) + half * ((BH * 128) >> 4);
+                if (one) {
 #pragma unroll
-                for (int c = 0; c < S::CB; ++c)
+                    for (int c = 0; c < S::CB; ++c)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_ss(to, q + ((c * BM * 128) >> 4) + 2 * k, k1 + ((c * BN * 128) >> 4) + 2 * k, id_s,
-                                   c + k != 0);
-                tc::mma_commit(&bar.s_full[t][half]);
-                if (half == 1 && t == TILES - 1) tc::mma_commit(&bar.k_empty[st]);
-            }
-        };
-        auto product_o = [&](int t, int j) {
-            const int half = j & 1, st = (j >> 1) % STAGES;
-            const uint32_t v1 = v0 + st * (S::V_BYTES >> 4) + half * ((D * 128) >> 4);
-            const uint32_t p = tm + t * BN + half * BH, to = tm + 2 * BN + t * D;
-            if (one) {
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_ss(t_s + half * BH, q0 + ((c * BM * 128) >> 4) + 2 * k,
+                                       k1 + ((c * BN * 128) >> 4) + 2 * k, id_s, c + k != 0);
+                    tc::mma_commit(&bar.s_full[t][half]);
+                    if (half == 1) tc::mma_commit(&bar.k_empty[st]);
+                }
+            };
+            auto product_o = [&](int j) {
+                const int half = j & 1, st = (j >> 1) % STAGES;
+                const uint32_t v1 = v0 + st * (S::V_BYTES >> 4) + half * ((D * 128) >> 4);
+                if (one) {
 #pragma unroll
-                for (int k = 0; k < BH / 16; ++k)
-                    mma_f16_ts(to, p + k * 8, v1 + 2 * k, id_o, k != 0 ? 1u : (uint32_t)j);
-                tc::mma_commit(&bar.o_done[t]);
-                if (half == 1 && t == TILES - 1) tc::mma_commit(&bar.v_empty[st]);
-            }
-        };
-        if (issuer) {
+                    for (int k = 0; k < BH / 16; ++k)
+                        mma_f16_ts(t_o, t_s + half * BH + k * 8, v1 + 2 * k, id_o, k != 0 ? 1u : (uint32_t)j);
+                    tc::mma_commit(&bar.o_done[t][half]);
+                    if (half == 1) tc::mma_commit(&bar.v_empty[st]);
+                }
+            };
             bool ok = true;
             if (stall) ok = wait_all(&bar.never, 0);  // test hook
             if (halves > 0) {
                 ok = ok && wait_all(&bar.k_full[0], 0);
                 if (ok) {
                     tc::tc_fence_after();
-                    for (int j = 0; j < 2; ++j)
-                        for (int t = 0; t < TILES; ++t) product_s(t, j);
+                    product_s(0);
+                    product_s(1);
                 }
             }
             for (int j = 0; ok && j < halves; ++j) {
                 const int i = j >> 1, half = j & 1;
-                if (half == 0) ok = wait_all(&bar.v_full[i % STAGES], (i / STAGES) & 1);
-                for (int t = 0; ok && t < TILES; ++t) {
-                    ok = wait_all(&bar.p_full[t][half], i & 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    product_o(t, j);
-                }
-                if (!ok || j + 2 >= halves) continue;
-                if (half == 0) ok = wait_all(&bar.k_full[(i + 1) % STAGES], ((i + 1) / STAGES) & 1);
-                for (int t = 0; ok && t < TILES; ++t) {
-                    ok = wait_all(&bar.o_done[t], half);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    product_s(t, j + 2);
-                }
+                ok = (half == 1 || wait_all(&bar.v_full[i % STAGES], (i / STAGES) & 1)) &&
+                     wait_all(&bar.p_full[t][half], i & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+                product_o(j);
+                if (j + 2 >= halves) continue;
+                ok = (half == 1 || wait_all(&bar.k_full[(i + 1) % STAGES], ((i + 1) / STAGES) & 1)) &&
+                     wait_all(&bar.o_done[t][half], i & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+                product_s(j + 2);
             }
             // Nothing may still read this block's memory when it leaves, also after an abort.
-            commit(&bar.done);
+            if (one) tc::mma_commit(&bar.done);
             int zero = 0;
             tc::mbar_wait_bounded(&bar.done, 0, &zero, limit);
         }
