@@ -7,7 +7,7 @@
 //   S = Q K^T   (binary16 x binary16 -> fp32 in tensor memory)
 //   p_j = 2^(k S_j + e - ref), rounded to binary16 into tensor memory over S
 //   O += P V    (P from tensor memory, O stays there)
-// K and V come from the paged 4-bit cache: four warps read the codes into registers (a step ahead) and
+// K and V come from the paged 4-bit cache: bulk copies bring the codes, and four warps
 // write the values in binary16 in the layout the tensor core reads: K rows of keys, V transposed (rows
 // of values, so that both operands are contiguous along the sum), 128-byte swizzled.  The order of
 // values inside each group of eight is that in which a word's nibbles come out; Q is laid out alike.
@@ -20,7 +20,8 @@
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
 //   warps 8-11       unpack K, V; copy the scales
-//   warps 12, 13     issue the products of tile 0, 1 (12 owns tensor memory; 14 and 15 fill the register group)
+//   warps 12, 13     issue the products of tile 0, 1 (12 owns tensor memory)
+//   warp 14          copies codes and scales from the cache (15 fills the register group)
 // One tile's products run under the other's softmax.
 //
 // A row's reference is raised (and O scaled down) only when the weights of a step might not fit
@@ -74,9 +75,14 @@ struct Shape {
     static constexpr int VB = D == 64 ? 4 : 8;           // bytes of a value row that a thread transposes
     static constexpr int Q_BYTES = BM * D * 2, K_BYTES = BN * D * 2, V_BYTES = BN * D * 2;
     static constexpr int K_AT = TILES * Q_BYTES, V_AT = K_AT + STAGES * K_BYTES, SC_AT = V_AT + STAGES * V_BYTES;
-    static constexpr int BAR_AT = SC_AT + RING * (BN * 2 + 36) + 16;
-    static constexpr int SMEM = BAR_AT + 256;
-    static_assert(BAR_AT % 16 == 0, "alignment");
+    // Codes and scales as they come from the cache: keys one behind the other, values in eights of keys 16
+    // bytes apart, so that the transposing reads meet no bank twice.
+    static constexpr int V_STRIDE = 8 * ROW + 16;
+    static constexpr int KC_AT = SC_AT + RING * 36 + BN * 4 + 16 - (RING * 36) % 16, VC_AT = KC_AT + BN * ROW;
+    static constexpr int KS_AT = VC_AT + (BN / 8) * V_STRIDE, VS_AT = KS_AT + BN * 4;
+    static constexpr int BAR_AT = VS_AT + BN * 4;
+    static constexpr int SMEM = BAR_AT + 288;
+    static_assert(KC_AT % 16 == 0 && VC_AT % 16 == 0 && KS_AT % 16 == 0 && BAR_AT % 16 == 0, "alignment");
     static constexpr int OPAD = D + 4;
     static_assert(TILES * BM * OPAD * 4 <= BAR_AT, "finished rows lie over the operands");
     static_assert(SMEM <= 232448, "shared memory");
@@ -86,13 +92,15 @@ struct Shape {
 struct Bars {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t scales[RING];
+    uint64_t ratios;
+    uint64_t kc_full, kc_empty, vc_full, vc_empty;  // codes and scales as they come from the cache
     uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES][2];  // by halves of a step
     uint64_t done, never;
     uint32_t tmem;
     int abort;
     int pmin[TILES], pmax[TILES], least[TILES];
 };
-static_assert(sizeof(Bars) <= 256, "barrier area");
+static_assert(sizeof(Bars) <= 288, "barrier area");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort, long long limit) {
     if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait_bounded(bar, parity, abort, limit)) return true;
@@ -163,6 +171,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
 }
 __device__ __forceinline__ void soft_bar() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory"); }
 
@@ -278,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* factor_k = reinterpret_cast<float4*>(smem + S::SC_AT);      // [RING] k of the step's four 32s of keys
     float4* power_v = factor_k + RING;                                   // [RING] e
     uint32_t* gone = reinterpret_cast<uint32_t*>(power_v + RING);        // [RING] 16s of keys that are not there
-    __half* ratio_v = reinterpret_cast<__half*>(gone + RING);            // [RING][BN]
+    __half* ratio_v = reinterpret_cast<__half*>(smem + S::KC_AT - BN * 4);  // [2][BN]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in all lanes
     const int G = a.q_heads / a.kv_heads;
@@ -317,6 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar.pmin[i] = bar.least[i] = 0x7fffffff;
             bar.pmax[i] = -1;
         }
+        tc::mbar_init(&bar.ratios, kUnpackThreads);
+        tc::mbar_init(&bar.kc_full, 1);
+        tc::mbar_init(&bar.vc_full, 1);
+        tc::mbar_init(&bar.kc_empty, kUnpackThreads);
+        tc::mbar_init(&bar.vc_empty, kUnpackThreads);
         tc::mbar_init(&bar.done, TILES);
         tc::mbar_init(&bar.never, 1);
         bar.abort = 0;
@@ -487,62 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kSoftWarps + kUnpackWarps) {
         // ------------------------------------------------------------------------------- unpack
         fewer_registers<kUnpackRegs>();
-        // A warp's lanes 0-7 hold where the step's eight 16s of keys lie in the pool.
         const int w = warp - kSoftWarps, l8 = lane & 7, l4 = lane >> 3, u = w * 32 + lane;
         const Nibbles nib;
-        auto find = [&](int i) -> uint32_t {
-            uint32_t at = kNowhere;
-            if (i < n && lane < 8) {
-                const int j = block_of(i) * BN + lane * 16;
-                if (j < range.limit) {
-                    const int page = table[j >> a.log_page];
-                    if ((uint32_t)page < (uint64_t)a.n_pages)
-                        at = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & ((1 << a.log_page) - 1))) >> 4);
-                }
-            }
-            return at;
-        };
-        uint4 kq[S::CH];
-        uint2 vq[8];
-        float ks, vs;
-        auto row_at = [&](uint32_t place, int kg) { return (uint64_t)place * 16 + (kg & 1) * 8; };
-        auto load_k = [&](uint32_t places, int i) {
-#pragma unroll
-            for (int q = 0; q < S::CH; ++q) {
-                const int v = (w * S::CH + q) * 4 + l4, kg = v / S::CH, cc = v % S::CH;
-                const uint32_t place = __shfl_sync(0xffffffffu, places, kg >> 1);
-                kq[q] = make_uint4(0u, 0u, 0u, 0u);
-                if (place != kNowhere && QIFT_CK((int64_t)place * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page))
-                    kq[q] = __ldg(reinterpret_cast<const uint4*>(a.k_cache + (row_at(place, kg) + l8) * S::ROW + cc * 16));
-            }
-            const uint32_t place = __shfl_sync(0xffffffffu, places, u >> 4);
-            ks = vs = 0.0f;
-            if (place != kNowhere && block_of(i) * BN + u < range.limit) {
-                ks = __ldg(a.k_scales + (uint64_t)place * 16 + (u & 15));
-                vs = __ldg(a.v_scales + (uint64_t)place * 16 + (u & 15));
-            }
-        };
         const int v_kg = l8 + 8 * (w & 1), v_dc = l4 + 4 * (w >> 1);  // eight keys, VB bytes of each
-        auto load_v = [&](uint32_t places) {
-            const uint32_t place = __shfl_sync(0xffffffffu, places, v_kg >> 1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                vq[j] = make_uint2(0u, 0u);
-                if (place != kNowhere && QIFT_CK((int64_t)place * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page)) {
-                    const uint8_t* p = a.v_cache + (row_at(place, v_kg) + j) * S::ROW + v_dc * S::VB;
-                    if constexpr (S::VB == 8) vq[j] = __ldg(reinterpret_cast<const uint2*>(p));
-                    else vq[j].x = __ldg(reinterpret_cast<const uint32_t*>(p));
-                }
-            }
-        };
-        uint32_t now = find(0), next = find(1);
-        load_k(now, 0);
-        load_v(now);
         for (int i = 0; i < n; ++i) {
             const int st = i % STAGES, ring = i % RING;
-            if (i >= STAGES &&
-                !__all_sync(0xffffffffu, wait(&bar.k_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
+            if (!__all_sync(0xffffffffu, wait(&bar.kc_full, i & 1, &bar.abort, limit) &&
+                                             (i < STAGES || wait(&bar.k_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit))))
                 break;
+            const bool is = block_of(i) * BN + u < range.limit && !((gone[ring] >> (u >> 4)) & 1u);
+            const float ks = is ? reinterpret_cast<const float*>(smem + S::KS_AT)[u] : 0.0f;
+            const float vs = is ? reinterpret_cast<const float*>(smem + S::VS_AT)[u] : 0.0f;
             // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free.
             // This warp's 32 keys are a chunk: m = 7 s by a power of two, that of the largest.
             const float mk = scale7(ks), mv = scale7(vs);
@@ -554,36 +527,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int ek = exponent(most_k), ev = exponent(most_v);
             const uint32_t rk = __half_as_ushort(__float2half_rn(mk * power(-ek)));
-            ratio_v[ring * BN + u] = __float2half_rn(mv * power(-ev));
-            const uint32_t away = __ballot_sync(0xffffffffu, lane < 8 && now == kNowhere);
+            ratio_v[(i & 1) * BN + u] = __float2half_rn(mv * power(-ev));  // that of step i - 2 is read: `ratios` of step i - 1
+            tc::mbar_arrive(&bar.ratios);
             if (lane == 0) {
                 reinterpret_cast<float*>(factor_k + ring)[w] = power(ek) * (a.scale_log2 * (1.0f / 7.0f));
                 reinterpret_cast<float*>(power_v + ring)[w] = (float)ev;
-                if (w == 0) gone[ring] = away;
             }
             tc::mbar_arrive(&bar.scales[ring]);
             const uint32_t k_to = base32 + S::K_AT + st * S::K_BYTES;
+            // 16-byte piece cc of key kk of this warp's 32 holds groups 4 cc .. 4 cc + 3 of eight values.  Lanes read
+            // side by side; half of them write their groups in another order, so that no bank is met twice.
 #pragma unroll
             for (int q = 0; q < S::CH; ++q) {
-                const int v = (w * S::CH + q) * 4 + l4, kg = v / S::CH, cc = v % S::CH;
-                const uint32_t words[4] = {kq[q].x, kq[q].y, kq[q].z, kq[q].w};
-                const uint32_t r1 = __shfl_sync(0xffffffffu, rk, kg * 8 + l8 - 32 * w), r2 = r1 | (r1 << 16);
+                const int piece = q * 32 + lane, kk = piece / S::CH, cc = piece % S::CH;
+                const uint4 x4 = *reinterpret_cast<const uint4*>(smem + S::KC_AT + (w * 32 + kk) * S::ROW + cc * 16);
+                const bool swap = (cc >> 1) & 1;
+                const uint32_t words[4] = {swap ? x4.z : x4.x, swap ? x4.w : x4.y, swap ? x4.x : x4.z, swap ? x4.y : x4.w};
+                const uint32_t r1 = __shfl_sync(0xffffffffu, rk, kk), r2 = r1 | (r1 << 16);
+                const uint32_t to = k_to + (w * 32 + kk) * 128 + (cc >> 1) * (BN * 128);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int c = cc * 4 + e;  // which group of eight values
+                    const int c = (cc & 1) * 4 + (swap ? e ^ 2 : e);
                     const uint32_t x = words[e], y = words[e] >> 8;
-                    sts128(k_to + (c >> 3) * (BN * 128) + (kg * 8 + l8) * 128 + (((c & 7) ^ l8) << 4),
-                           mulh2(nib.lo(x), r2), mulh2(nib.hi(x), r2), mulh2(nib.lo(y), r2), mulh2(nib.hi(y), r2));
+                    sts128(to + ((c ^ (kk & 7)) << 4), mulh2(nib.lo(x), r2), mulh2(nib.hi(x), r2), mulh2(nib.lo(y), r2),
+                           mulh2(nib.hi(y), r2));
                 }
             }
-            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&bar.kc_empty);
             tc::mbar_arrive(&bar.k_full[st]);
-            if (i + 1 < n) load_k(next, i + 1);  // behind the fence, which would wait for the loads
+            if (!__all_sync(0xffffffffu, wait(&bar.vc_full, i & 1, &bar.abort, limit) &&
+                                             wait(&bar.ratios, i & 1, &bar.abort, limit)))
+                break;
             if (i >= STAGES &&
                 !__all_sync(0xffffffffu, wait(&bar.v_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
                 break;
-            asm volatile("bar.sync 2, %0;" ::"n"(kUnpackThreads) : "memory");  // all four warps' ratios
-            const uint4 rv4 = *reinterpret_cast<const uint4*>(ratio_v + ring * BN + v_kg * 8);
+            const uint4 rv4 = *reinterpret_cast<const uint4*>(ratio_v + (i & 1) * BN + v_kg * 8);
+            uint32_t vq[8][S::VB / 4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint8_t* from = smem + S::VC_AT + v_kg * S::V_STRIDE + j * S::ROW + v_dc * S::VB;
+                if constexpr (S::VB == 8) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(from);
+                    vq[j][0] = x.x, vq[j][1] = x.y;
+                } else {
+                    vq[j][0] = *reinterpret_cast<const uint32_t*>(from);
+                }
+            }
             const uint32_t rv[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
             const uint32_t v_to = base32 + S::V_AT + st * S::V_BYTES + (v_kg >> 3) * (D * 128);
 #pragma unroll
@@ -593,8 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t x[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] = prmt(wd ? vq[2 * k].y : vq[2 * k].x, wd ? vq[2 * k + 1].y : vq[2 * k + 1].x,
-                                    hf ? 0x7632u : 0x5410u);
+                        x[k] = prmt(vq[2 * k][wd], vq[2 * k + 1][wd], hf ? 0x7632u : 0x5410u);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int d8 = 4 * hf + 2 * e;  // value's place among the word's eight
@@ -607,11 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) x[k] >>= 8;
                     }
                 }
-            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&bar.vc_empty);
             tc::mbar_arrive(&bar.v_full[st]);
-            if (i + 1 < n) load_v(next);
-            now = next;
-            next = find(i + 2);
         }
     } else {
         fewer_registers<kIssueRegs>();
@@ -665,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (halves > 0) {
                 ok = ok && wait_all(&bar.k_full[0], 0);
                 if (ok) {
+                    tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
                     product_s(0);
                     product_s(1);
@@ -675,12 +661,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = (half == 1 || wait_all(&bar.v_full[i % STAGES], (i / STAGES) & 1)) &&
                      wait_all(&bar.p_full[t][half], i & 1);
                 if (!ok) break;
+                if (half == 0) tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 product_o(j);
                 if (j + 2 >= halves) continue;
                 ok = (half == 1 || wait_all(&bar.k_full[(i + 1) % STAGES], ((i + 1) / STAGES) & 1)) &&
                      wait_all(&bar.o_done[t][half], i & 1);
                 if (!ok) break;
+                if (half == 0) tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 product_s(j + 2);
             }
@@ -688,6 +676,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one) tc::mma_commit(&bar.done);
             int zero = 0;
             tc::mbar_wait_bounded(&bar.done, 0, &zero, limit);
+        } else if (t == TILES) {
+            // ---------------------------------------------------------------------------- loader
+            // Lanes 0-7 have one 16 of keys each: it lies in one page, one head's rows one behind the other.
+            // Copies instead of loads by the unpacking warps: those waited for their loads at every
+            // fence, and for the page numbers, 2800 cycles of a step's 5000.
+            auto find = [&](int i) -> uint32_t {
+                uint32_t at = kNowhere;
+                if (i < n && lane < 8) {
+                    const int j = block_of(i) * BN + lane * 16;
+                    if (j < range.limit) {
+                        const int page = table[j >> a.log_page];
+                        if ((uint32_t)page < (uint64_t)a.n_pages)
+                            at = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & ((1 << a.log_page) - 1))) >> 4);
+                    }
+                    if (!QIFT_CK(at == kNowhere || (int64_t)at * 16 + 16 <= (a.n_pages * a.kv_heads) << a.log_page)) at = kNowhere;
+                }
+                return at;
+            };
+            bool ok = true;
+            uint32_t at = find(0);
+            int k_sent = 0, v_sent = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint32_t away = __ballot_sync(0xffffffffu, lane < 8 && at == kNowhere);
+                const uint32_t count = 8 - __popc(away);
+                ok = __all_sync(0xffffffffu, i == 0 || wait(&bar.kc_empty, (i - 1) & 1, &bar.abort, limit));
+                if (!ok) break;
+                if (lane == 0) {
+                    gone[i % RING] = away;
+                    tc::mbar_arrive_expect_tx(&bar.kc_full, count * (16 * S::ROW + 128));
+                }
+                __syncwarp();
+                if (at != kNowhere) {
+                    bulk_copy(base32 + S::KC_AT + lane * 16 * S::ROW, a.k_cache + (uint64_t)at * (16 * S::ROW), 16 * S::ROW,
+                              &bar.kc_full);
+                    bulk_copy(base32 + S::KS_AT + lane * 64, a.k_scales + (uint64_t)at * 16, 64, &bar.kc_full);
+                    bulk_copy(base32 + S::VS_AT + lane * 64, a.v_scales + (uint64_t)at * 16, 64, &bar.kc_full);
+                }
+                k_sent = i + 1;
+                ok = __all_sync(0xffffffffu, i == 0 || wait(&bar.vc_empty, (i - 1) & 1, &bar.abort, limit));
+                if (!ok) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(&bar.vc_full, count * (16 * S::ROW));
+                __syncwarp();
+                if (at != kNowhere)
+                    for (int e = 0; e < 2; ++e)
+                        bulk_copy(base32 + S::VC_AT + (2 * lane + e) * S::V_STRIDE,
+                                  a.v_cache + (uint64_t)at * (16 * S::ROW) + e * 8 * S::ROW, 8 * S::ROW, &bar.vc_full);
+                v_sent = i + 1;
+                at = find(i + 1);
+            }
+            // Copies in flight land before the block leaves, also after an abort.
+            int zero = 0;
+            if (k_sent > 0) tc::mbar_wait_bounded(&bar.kc_full, (k_sent - 1) & 1, &zero, limit);
+            if (v_sent > 0) tc::mbar_wait_bounded(&bar.vc_full, (v_sent - 1) & 1, &zero, limit);
         }
     }
     tc::tc_fence_before();
