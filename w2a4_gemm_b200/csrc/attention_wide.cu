@@ -81,7 +81,7 @@ struct Shape {
     static constexpr int KC_AT = SC_AT + RING * 36 + BN * 4 + 16 - (RING * 36) % 16, VC_AT = KC_AT + BN * ROW;
     static constexpr int KS_AT = VC_AT + (BN / 8) * V_STRIDE, VS_AT = KS_AT + BN * 4;
     static constexpr int BAR_AT = VS_AT + BN * 4;
-    static constexpr int SMEM = BAR_AT + 288;
+    static constexpr int SMEM = BAR_AT + 320;
     static_assert(KC_AT % 16 == 0 && VC_AT % 16 == 0 && KS_AT % 16 == 0 && BAR_AT % 16 == 0, "alignment");
     static constexpr int OPAD = D + 4;
     static_assert(TILES * BM * OPAD * 4 <= BAR_AT, "finished rows lie over the operands");
@@ -93,6 +93,7 @@ struct Bars {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t scales[RING];
     uint64_t ratios;
+    uint64_t q_full[TILES];
     uint64_t kc_full, kc_empty, vc_full, vc_empty;  // codes and scales as they come from the cache
     uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES][2];  // by halves of a step
     uint64_t done, never;
@@ -100,7 +101,7 @@ struct Bars {
     int abort;
     int pmin[TILES], pmax[TILES], least[TILES];
 };
-static_assert(sizeof(Bars) <= 288, "barrier area");
+static_assert(sizeof(Bars) <= 320, "barrier area");
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort, long long limit) {
     if (tc::mbar_try_wait(bar, parity) || tc::mbar_wait_bounded(bar, parity, abort, limit)) return true;
@@ -327,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mbar_init(&bar.p_full[i][half], BM);
                 tc::mbar_init(&bar.o_done[i][half], 1);
             }
+            tc::mbar_init(&bar.q_full[i], BM);
             bar.pmin[i] = bar.least[i] = 0x7fffffff;
             bar.pmax[i] = -1;
         }
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     __syncthreads();
 
-    // ---- rows: position, and Q into shared memory
+    // ---- rows and their positions
     const int tile = warp >> 2, r = (warp & 3) * 32 + lane;  // of a softmax thread
     int64_t token = -1;
     int pos = -1, head = 0;
@@ -370,16 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicMin(&bar.least[tile], pos);
             if (pos >= 0) atomicMin(&bar.pmin[tile], pos), atomicMax(&bar.pmax[tile], pos);
         }
-        const __half* src = a.q + (token >= 0 ? token * a.q_stride + (int64_t)head * D : 0);
-        const uint32_t dst = base32 + tile * S::Q_BYTES + r * 128;
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (token >= 0) x = *reinterpret_cast<const uint4*>(src + c * 8);
-            sts128(dst + (c >> 3) * (BM * 128) + (((c & 7) ^ (r & 7)) << 4), prmt(x.x, x.z, 0x5410u),
-                   prmt(x.x, x.z, 0x7632u), prmt(x.y, x.w, 0x5410u), prmt(x.y, x.w, 0x7632u));
-        }
-        tc::fence_proxy_async_smem();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -396,6 +388,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------------------------ softmax
         more_registers<kSoftRegs>();
+        {  // Q of this warp's 32 rows: whole lines, a row over D / 8 lanes
+            constexpr int PIECES = D / 8, PER = 32 / PIECES;
+            const int64_t from = token >= 0 ? token * a.q_stride + (int64_t)head * D : -1;
+            const int c = lane % PIECES;
+            const uint32_t dst = base32 + tile * S::Q_BYTES + (c >> 3) * (BM * 128) + (warp & 3) * 32 * 128;
+#pragma unroll 8
+            for (int k0 = 0; k0 < 32; k0 += PER) {
+                const int k = k0 + lane / PIECES;
+                const int64_t at = __shfl_sync(0xffffffffu, from, k);
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (at >= 0) x = __ldg(reinterpret_cast<const uint4*>(a.q + at + c * 8));
+                sts128(dst + k * 128 + (((c & 7) ^ (k & 7)) << 4), prmt(x.x, x.z, 0x5410u), prmt(x.x, x.z, 0x7632u),
+                       prmt(x.y, x.w, 0x5410u), prmt(x.y, x.w, 0x7632u));
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&bar.q_full[tile]);
+        }
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + quarter + tile * BN, t_o = tmem + quarter + 2 * BN + tile * D;
         const int t_least = bar.least[tile], t_pmax = bar.pmax[tile];
@@ -459,47 +468,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0 && ok) ok = wait(&bar.o_done[tile][1], (n - 1) & 1, &bar.abort, limit);
         ok = __all_sync(0xffffffffu, ok);
         soft_bar();  // both tiles' products are done: the operands' memory is free
-        // Rows through shared memory, so that a warp finishes one together (rotation back, whole lines).
         ok = ok && !*reinterpret_cast<volatile int*>(&bar.abort);
         if (ok) {
+            // A thread finishes its row in registers (the rotation back needs no exchange), and a warp's rows go
+            // out through shared memory as whole lines.  A warp a row, with shuffles, took 19000 cycles a
+            // block, a quarter of the time of a block with a window of 1024 keys.
             tc::tc_fence_after();
-            float* rows = reinterpret_cast<float*>(smem) + (tile * BM + (warp & 3) * 32) * S::OPAD;
-#pragma unroll 1
+            float v[D];
+#pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
                 if (n > 0) {
                     tc::tmem_ld_32x32b_x32(t_o + 32 * c, x);
-                    tc::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = 0u;
+                    tmem_ld_wait_for(x);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4*>(rows + lane * S::OPAD + 32 * c + e) =
-                        make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                for (int e = 0; e < 32; ++e) v[32 * c + e] = n > 0 ? __uint_as_float(x[e]) : 0.0f;
+            }
+            const bool finish = deal.slots == 0;
+            const float by = finish ? (sum > 0.0f ? __fdiv_rn(1.0f, 7.0f * sum) : 0.0f) : 1.0f / 7.0f;
+#pragma unroll
+            for (int e = 0; e < D; ++e) v[e] *= by;
+            int64_t at = token >= 0 ? token * a.q_heads + head : -1;
+            if (finish) {
+                if (a.block) {
+#pragma unroll
+                    for (int hd = 1; hd < D; hd <<= 1) {
+                        if (a.block > hd) {
+#pragma unroll
+                            for (int e = 0; e < D; ++e) {
+                                if (e & hd) continue;
+                                const float x = v[e], y = v[e + hd];
+                                v[e] = x + y;
+                                v[e + hd] = x - y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < D; ++e) v[e] *= a.norm;
+                }
+                if (a.lse && token >= 0) a.lse[at] = sum > 0.0f ? 0.69314718056f * (ref + log2f(sum)) : -INFINITY;
+            } else if (token >= 0) {
+                at = at * deal.slots + (prefix ? split : deal.prefix_splits + split);
+                parts(a, deal.slots).ml[at] = make_float2(ref, sum);
+            }
+            float* rows = reinterpret_cast<float*>(smem) + (tile * BM + (warp & 3) * 32) * S::OPAD;
+            const bool narrow = finish && a.f16;
+            if (narrow) {
+#pragma unroll
+                for (int e = 0; e < D; e += 8) {
+                    __half2 x[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x[q] = __floats2half2_rn(v[e + 2 * q], v[e + 2 * q + 1]);
+                    *reinterpret_cast<uint4*>(rows + lane * S::OPAD + e / 2) = *reinterpret_cast<const uint4*>(x);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < D; e += 4)
+                    *reinterpret_cast<float4*>(rows + lane * S::OPAD + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
             __syncwarp();
-            constexpr int E = D / 32;
-            for (int k = 0; k < 32; ++k) {
-                const int64_t tk = __shfl_sync(0xffffffffu, token, k);
-                const int hd = __shfl_sync(0xffffffffu, head, k);
-                const float M = __shfl_sync(0xffffffffu, ref, k), L = __shfl_sync(0xffffffffu, sum, k);
-                if (tk < 0) continue;
-                float acc[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = rows[k * S::OPAD + lane * E + e] * (1.0f / 7.0f);
-                if (deal.slots == 0) {
-                    finish_row<D>(a, acc, M, L, tk, hd, lane);
-                } else {
-                    const Parts p = parts(a, deal.slots);
-                    const int64_t at = (tk * a.q_heads + hd) * deal.slots + (prefix ? split : deal.prefix_splits + split);
-                    if (lane == 0) p.ml[at] = make_float2(M, L);
-                    if (L > 0.0f) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) p.o[at * D + lane * E + e] = acc[e];
-                    }
-                }
+            const int pieces = narrow ? D / 8 : D / 4;  // 16 bytes each
+            uint4* to = finish ? static_cast<uint4*>(a.out) : reinterpret_cast<uint4*>(parts(a, deal.slots).o);
+#pragma unroll 4
+            for (int x = lane; x < 32 * pieces; x += 32) {
+                const int k = x / pieces, c = x % pieces;
+                const int64_t row = __shfl_sync(0xffffffffu, at, k);
+                if (row >= 0) to[row * pieces + c] = *reinterpret_cast<const uint4*>(rows + k * S::OPAD + c * 4);
             }
         }
     } else if (warp < kSoftWarps + kUnpackWarps) {
@@ -648,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             if (stall) ok = wait_all(&bar.never, 0);  // test hook
             if (halves > 0) {
-                ok = ok && wait_all(&bar.k_full[0], 0);
+                ok = ok && wait_all(&bar.q_full[t], 0) && wait_all(&bar.k_full[0], 0);
                 if (ok) {
                     tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
