@@ -393,14 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t from = token >= 0 ? token * a.q_stride + (int64_t)head * D : -1;
             const int c = lane % PIECES;
             const uint32_t dst = base32 + tile * S::Q_BYTES + (c >> 3) * (BM * 128) + (warp & 3) * 32 * 128;
-#pragma unroll 8
-            for (int k0 = 0; k0 < 32; k0 += PER) {
-                const int k = k0 + lane / PIECES;
-                const int64_t at = __shfl_sync(0xffffffffu, from, k);
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (at >= 0) x = __ldg(reinterpret_cast<const uint4*>(a.q + at + c * 8));
-                sts128(dst + k * 128 + (((c & 7) ^ (k & 7)) << 4), prmt(x.x, x.z, 0x5410u), prmt(x.x, x.z, 0x7632u),
-                       prmt(x.y, x.w, 0x5410u), prmt(x.y, x.w, 0x7632u));
+            uint4 x[32 / PER];  // all loads in flight at once
+#pragma unroll
+            for (int q = 0; q < 32 / PER; ++q) {
+                const int64_t at = __shfl_sync(0xffffffffu, from, q * PER + lane / PIECES);
+                x[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (at >= 0) x[q] = __ldg(reinterpret_cast<const uint4*>(a.q + at + c * 8));
+            }
+#pragma unroll
+            for (int q = 0; q < 32 / PER; ++q) {
+                const int k = q * PER + lane / PIECES;
+                sts128(dst + k * 128 + (((c & 7) ^ (k & 7)) << 4), prmt(x[q].x, x[q].z, 0x5410u),
+                       prmt(x[q].x, x[q].z, 0x7632u), prmt(x[q].y, x[q].w, 0x5410u), prmt(x[q].y, x[q].w, 0x7632u));
             }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&bar.q_full[tile]);
@@ -470,71 +474,101 @@ __global__ void __launch_bounds__(kThreads, 1)
         soft_bar();  // both tiles' products are done: the operands' memory is free
         ok = ok && !*reinterpret_cast<volatile int*>(&bar.abort);
         if (ok) {
-            // A thread finishes its row in registers (the rotation back needs no exchange), and a warp's rows go
-            // out through shared memory as whole lines.  A warp a row, with shuffles, took 19000 cycles a
-            // block, a quarter of the time of a block with a window of 1024 keys.
+            // A thread finishes its row (the rotation back needs no exchange), 32 values at a time and then
+            // across those, and a warp's rows go out through shared memory as whole lines.  A warp a row, with
+            // shuffles, took 19000 cycles a block, a quarter of the time of a block with a window of 1024 keys; a
+            // row in registers, all of it unrolled, 9000, most of them for fetching the instructions.
             tc::tc_fence_after();
-            float v[D];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                if (n > 0) {
-                    tc::tmem_ld_32x32b_x32(t_o + 32 * c, x);
-                    tmem_ld_wait_for(x);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[32 * c + e] = n > 0 ? __uint_as_float(x[e]) : 0.0f;
-            }
             const bool finish = deal.slots == 0;
-            const float by = finish ? (sum > 0.0f ? __fdiv_rn(1.0f, 7.0f * sum) : 0.0f) : 1.0f / 7.0f;
-#pragma unroll
-            for (int e = 0; e < D; ++e) v[e] *= by;
+            const int block = finish ? a.block : 0;
+            const float by = (finish ? (sum > 0.0f ? __fdiv_rn(1.0f, 7.0f * sum) : 0.0f) : 1.0f / 7.0f) *
+                             (block ? a.norm : 1.0f);
             int64_t at = token >= 0 ? token * a.q_heads + head : -1;
             if (finish) {
-                if (a.block) {
-#pragma unroll
-                    for (int hd = 1; hd < D; hd <<= 1) {
-                        if (a.block > hd) {
-#pragma unroll
-                            for (int e = 0; e < D; ++e) {
-                                if (e & hd) continue;
-                                const float x = v[e], y = v[e + hd];
-                                v[e] = x + y;
-                                v[e + hd] = x - y;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < D; ++e) v[e] *= a.norm;
-                }
                 if (a.lse && token >= 0) a.lse[at] = sum > 0.0f ? 0.69314718056f * (ref + log2f(sum)) : -INFINITY;
             } else if (token >= 0) {
                 at = at * deal.slots + (prefix ? split : deal.prefix_splits + split);
                 parts(a, deal.slots).ml[at] = make_float2(ref, sum);
             }
             float* rows = reinterpret_cast<float*>(smem) + (tile * BM + (warp & 3) * 32) * S::OPAD;
-            const bool narrow = finish && a.f16;
-            if (narrow) {
+            float* mine = rows + lane * S::OPAD;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
 #pragma unroll
-                for (int e = 0; e < D; e += 8) {
-                    __half2 x[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) x[q] = __floats2half2_rn(v[e + 2 * q], v[e + 2 * q + 1]);
-                    *reinterpret_cast<uint4*>(rows + lane * S::OPAD + e / 2) = *reinterpret_cast<const uint4*>(x);
+                for (int e = 0; e < 32; ++e) x[e] = 0u;
+                if (n > 0) {
+                    tc::tmem_ld_32x32b_x32(t_o + 32 * c, x);
+                    tmem_ld_wait_for(x);
                 }
-            } else {
+                float v[32];
 #pragma unroll
-                for (int e = 0; e < D; e += 4)
-                    *reinterpret_cast<float4*>(rows + lane * S::OPAD + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(x[e]) * by;
+#pragma unroll
+                for (int hd = 1; hd < 32; hd <<= 1) {
+                    if (block > hd) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (e & hd) continue;
+                            const float y = v[e], z = v[e + hd];
+                            v[e] = y + z;
+                            v[e + hd] = y - z;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(mine + 32 * c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+            if (block > 32) {
+#pragma unroll 1
+                for (int e = 0; e < 32; e += 4) {
+                    float4 v[D / 32];
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) v[c] = *reinterpret_cast<const float4*>(mine + 32 * c + e);
+#pragma unroll
+                    for (int hd = 1; hd < D / 32; hd <<= 1) {
+                        if (block > 32 * hd) {
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                if (c & hd) continue;
+                                const float4 y = v[c], z = v[c + hd];
+                                v[c] = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+                                v[c + hd] = make_float4(y.x - z.x, y.y - z.y, y.z - z.z, y.w - z.w);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) *reinterpret_cast<float4*>(mine + 32 * c + e) = v[c];
+                }
             }
             __syncwarp();
-            const int pieces = narrow ? D / 8 : D / 4;  // 16 bytes each
-            uint4* to = finish ? static_cast<uint4*>(a.out) : reinterpret_cast<uint4*>(parts(a, deal.slots).o);
+            if (finish && a.f16) {
+                constexpr int PIECES = D / 8, PER = 32 / PIECES;  // of 16 bytes
+                const int c = lane % PIECES;
 #pragma unroll 4
-            for (int x = lane; x < 32 * pieces; x += 32) {
-                const int k = x / pieces, c = x % pieces;
-                const int64_t row = __shfl_sync(0xffffffffu, at, k);
-                if (row >= 0) to[row * pieces + c] = *reinterpret_cast<const uint4*>(rows + k * S::OPAD + c * 4);
+                for (int k0 = 0; k0 < 32; k0 += PER) {
+                    const int k = k0 + lane / PIECES;
+                    const int64_t row = __shfl_sync(0xffffffffu, at, k);
+                    const float4 x = *reinterpret_cast<const float4*>(rows + k * S::OPAD + c * 8);
+                    const float4 y = *reinterpret_cast<const float4*>(rows + k * S::OPAD + c * 8 + 4);
+                    const __half2 h[4] = {__floats2half2_rn(x.x, x.y), __floats2half2_rn(x.z, x.w), __floats2half2_rn(y.x, y.y),
+                                          __floats2half2_rn(y.z, y.w)};
+                    if (row >= 0)
+                        *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + row * D + c * 8) = *reinterpret_cast<const uint4*>(h);
+                }
+            } else {
+                float* to = finish ? static_cast<float*>(a.out) : parts(a, deal.slots).o;
+                constexpr int PIECES = D / 4, PER = 32 / PIECES;
+                const int c = lane % PIECES;
+#pragma unroll 4
+                for (int k0 = 0; k0 < 32; k0 += PER) {
+                    const int k = k0 + lane / PIECES;
+                    const int64_t row = __shfl_sync(0xffffffffu, at, k);
+                    if (row >= 0)
+                        *reinterpret_cast<float4*>(to + row * D + c * 4) =
+                            *reinterpret_cast<const float4*>(rows + k * S::OPAD + c * 4);
+                }
             }
         }
     } else if (warp < kSoftWarps + kUnpackWarps) {
