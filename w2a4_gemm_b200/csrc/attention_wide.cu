@@ -219,9 +219,14 @@ struct View {
     int hi, lo, sinks;   // key j counts if j <= hi and (j > lo or j < sinks)
     int j0;              // position of the step's first key
     uint32_t gone;       // 16s of keys that are not there
-    __device__ __forceinline__ bool sees(int k) const {
-        const int j = j0 + k;
-        return j <= hi && (j > lo || j < sinks) && !((gone >> (k >> 4)) & 1u);
+    // The keys first .. first + 31 of the step that count, a bit each.
+    __device__ __forceinline__ uint32_t bits(int first) const {
+        const int j = j0 + first;
+        const uint32_t g = (gone >> (first >> 4)) & 3u;
+        return up_to(hi - j) & (~up_to(lo - j) | up_to(sinks - 1 - j)) & ~((g & 1u ? 0xFFFFu : 0u) | (g & 2u ? 0xFFFF0000u : 0u));
+    }
+    __device__ __forceinline__ static uint32_t up_to(int k) {  // bits 0 .. k
+        return k < 0 ? 0u : k >= 31 ? 0xFFFFFFFFu : (2u << k) - 1u;
     }
 };
 
@@ -242,13 +247,14 @@ __device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[2], cons
         if (c + 1 < BH / 32) tc::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), in[(c + 1) & 1]);
         const uint64_t k2 = pack2(k[c], k[c]), off = pack2(e[c] - ref, e[c] - ref);
         uint64_t sum = pack2(0.0f, 0.0f);
+        const uint32_t seen = MASK ? view.bits(first + c * 32) : 0u;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float u0, u1;
             unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), k2, off), u0, u1);
             if (MASK) {
-                u0 = view.sees(first + c * 32 + 2 * i) ? u0 : -INFINITY;
-                u1 = view.sees(first + c * 32 + 2 * i + 1) ? u1 : -INFINITY;
+                u0 = seen & (1u << (2 * i)) ? u0 : -INFINITY;
+                u1 = seen & (2u << (2 * i)) ? u1 : -INFINITY;
             }
             const float w0 = ex2(u0), w1 = ex2(u1);
             sum = add2(sum, pack2(w0, w1));
@@ -273,10 +279,11 @@ __device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[2], co
         uint32_t x[32];
         tc::tmem_ld_32x32b_x32(taddr + 32 * c, x);
         tmem_ld_wait_for(x);
+        const uint32_t seen = mask ? view.bits(first + c * 32) : 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const float u = __fmaf_rn(__uint_as_float(x[i]), k[c], e[c]);
-            if (!mask || view.sees(first + c * 32 + i)) top = fmaxf(top, u);
+            if (seen & (1u << i)) top = fmaxf(top, u);
         }
     }
     return top;
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ref = kNone, sum = 0.0f;
         View view;
         view.hi = min(pos, base + range.limit - 1);
-        view.lo = a.window ? pos - a.window : -1;
+        view.lo = a.window ? max(pos - a.window, -1) : -1;
         view.sinks = a.sinks;
         bool ok = true;
         for (int i = 0; ok && i < n; ++i) {
