@@ -56,6 +56,12 @@ qift_status qift_debug_set_pdl(int32_t enable);
  * only the calls that thread makes. */
 qift_status qift_debug_set_linear_path(int32_t path);
 
+/* Pin the kernel that qift_paged_attention uses for all rows: 0 = automatic (the one expected to take
+ * less time), 1 = the streaming kernel (mma.sync, 8 or 16 rows a block), 2 = the one for many rows (tcgen05,
+ * 256 rows a block; head_dim 64 and 128, other calls return QIFT_ERR_UNSUPPORTED).  Per host thread;
+ * qift_paged_attention_workspace answers for the pinned kernel. */
+qift_status qift_debug_set_attention_path(int32_t path);
+
 /* 1 in the bounds-checked build of the library (compiled with -DQIFT_CHECK, for tests), 0 in
  * the normal build.  In the checked build every global index, bulk-copy range, tensor-map
  * coordinate and tensor-memory address a kernel computes is tested against the extent its

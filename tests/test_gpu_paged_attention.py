@@ -8,10 +8,9 @@ A = sum_j w_j |v_j|:
   * a score's error e_u moves the weights by at most 2 e_u relative: the product adds D + D/2 * 72-fold values in
     groups of 16, each addition off by at most 2^-22 of partial sums that stay under 80 sum|q|, so
     e_u <= (D/16 + 1) 2^-22 80 sum|q| max_j s_j scale; the 2^u, scalings and sums add under 2^-17 relative;
-  * where a kv head has 64 rows or more (WIDE: prompts, a prefix that many rows share; head_dim up to 128), keys and
-    values are binary16 products of the code and the row's magnitude: 2^-12 of each more, so A grows by 2^-12 A (and
-    what lies under 2^-14 of the largest value of its 32 keys by 2^-25 of that), and a score is off by up to
-    2^-12 sum|q_d k_d| scale <= 2^-12 sum|q| 7 max s scale more;
+  * the kernel for many rows ("wide") has keys and values as binary16 products of the code and the row's magnitude:
+    2^-12 of each more, so the error grows by 2^-12 A (and for what lies under 2^-14 of the largest value of its 32
+    keys by 2^-25 of that), and a score is off by up to 2^-12 sum|q_d k_d| scale <= 2^-12 sum|q| 7 max s scale more;
   * a binary16 result is off by 2^-11 of the value (2^-25 where it is subnormal).
 """
 import math
@@ -212,7 +211,7 @@ def make(q_lens, kv_lens, hq, hk, d, size, prefix=0, seed=0, gain=1.0):
 
 
 def reference(m, window=0, sinks=0, scale=None, prefix=None):
-    """The formula in 64 bits: (out in the cache's domain, lse, A, e_u) per row."""
+    """The formula in 64 bits: (out in the cache's domain, lse, A, sum|q| max s scale, largest |v|) per row."""
     kc, ks, vc, vs = m["cache"]
     pages, hk, size, half = kc.shape
     d = 2 * half
@@ -221,9 +220,8 @@ def reference(m, window=0, sinks=0, scale=None, prefix=None):
     scale = 1 / math.sqrt(d) if scale is None else scale
     out, A = torch.zeros(2, T, hq, d, dtype=torch.float64, device="cuda")
     lse = torch.full((T, hq), -math.inf, dtype=torch.float64, device="cuda")
-    e_u = torch.zeros(T, hq, dtype=torch.float64, device="cuda")
+    reach, v_max = torch.zeros(2, T, hq, dtype=torch.float64, device="cuda")
     cu, lens, P = m["cu_q"].tolist(), m["kv_lens"].tolist(), m["prefix"]
-    wide = d <= 128 and max(m["max_q"], T if P else 0) * (hq // hk) >= 64
     for b, n in enumerate(lens):
         nq = cu[b + 1] - cu[b]
         if not nq:
@@ -256,16 +254,29 @@ def reference(m, window=0, sinks=0, scale=None, prefix=None):
                 out[cu[b]:cu[b + 1], x], A[cu[b]:cu[b + 1], x] = w @ v, w @ v.abs()
                 lse[cu[b]:cu[b + 1], x] = l
                 s_max = torch.nan_to_num(k.abs().amax() / 7) if n else 0
-                e_u[cu[b]:cu[b + 1], x] = q[cu[b]:cu[b + 1], x].abs().sum(-1) * s_max * scale * (
-                    (d / 16 + 1) * 2.0 ** -22 * 80 + (7 * 2.0 ** -12 if wide else 0))
-                if wide and n:
-                    A[cu[b]:cu[b + 1], x] = 2 * A[cu[b]:cu[b + 1], x] + 2.0 ** -13 * torch.nan_to_num(v.abs().amax())
-    return out, lse, A, e_u
+                reach[cu[b]:cu[b + 1], x] = q[cu[b]:cu[b + 1], x].abs().sum(-1) * s_max * scale
+                v_max[cu[b]:cu[b + 1], x] = torch.nan_to_num(v.abs().amax()) if n else 0
+    return out, lse, A, reach, v_max
 
 
-def bound(A, e_u, ref, half):
-    t = A * (2.0 ** -12 + 2 * e_u[..., None] + 2.0 ** -17) + A.amax(-1, keepdim=True) * 2.0 ** -16
+def score_error(reach, d, wide):
+    return reach * ((d / 16 + 1) * 2.0 ** -22 * 80 + (7 * 2.0 ** -12 if wide else 0))
+
+
+def bound(A, reach, v_max, ref, half, wide):
+    t = A * ((2 if wide else 1) * 2.0 ** -12 + 2 * score_error(reach, A.shape[-1], wide)[..., None] + 2.0 ** -17)
+    t = t + A.amax(-1, keepdim=True) * 2.0 ** -16 + (v_max[..., None] * 2.0 ** -25 if wide else 0)
     return t + (2.0 ** -11 * ref.abs() + 2.0 ** -25 if half else 2.0 ** -22 * ref.abs() + 1e-38)
+
+
+def paths(m):
+    return ("stream", "wide") if m["q"].shape[-1] <= 128 else ("stream",)
+
+
+@pytest.fixture(autouse=True)
+def _automatic():
+    yield
+    qg.qift_debug_set_attention_path("auto")
 
 
 def call(m, **kw):
@@ -274,22 +285,28 @@ def call(m, **kw):
 
 
 def check(m, window=0, sinks=0, scale=None, dtypes=(torch.float32, torch.float16), **kw):
-    ref, lse, A, e_u = reference(m, window, sinks, scale)
+    """Both kernels on the same call."""
+    ref, lse, A, reach, v_max = reference(m, window, sinks, scale)
     cu = m["cu_q"].tolist()
-    for dt in dtypes:
-        out = torch.full(m["q"].shape, 77.0, device="cuda", dtype=dt)
-        l = torch.full(m["q"].shape[:2], 77.0, device="cuda")
-        call(m, window=window, sinks=sinks, scale=scale, out=out, out_dtype=dt, lse=l, **kw)
-        inside = slice(cu[0], cu[-1])
-        err = (out.double() - ref).abs()[inside]
-        tol = bound(A, e_u, ref, dt == torch.float16)[inside]
-        assert not torch.isnan(err).any()
-        assert (err <= tol).all(), (float((err / tol).max()), (err / tol).flatten(1).amax(1).tolist()[:40])
-        assert (out[:cu[0]] == 77).all() and (out[cu[-1]:] == 77).all()
-        none = lse[inside].isinf()
-        assert torch.equal(l[inside].isinf() & (l[inside] < 0), none)
-        assert (out[inside][none] == 0).all()
-        assert ((l.double() - lse)[inside][~none].abs() <= (e_u[inside] + 2.0 ** -16 + lse[inside].abs() * 2.0 ** -20)[~none]).all()
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        wide = path == "wide"
+        for dt in dtypes:
+            out = torch.full(m["q"].shape, 77.0, device="cuda", dtype=dt)
+            l = torch.full(m["q"].shape[:2], 77.0, device="cuda")
+            call(m, window=window, sinks=sinks, scale=scale, out=out, out_dtype=dt, lse=l, **kw)
+            inside = slice(cu[0], cu[-1])
+            err = (out.double() - ref).abs()[inside]
+            tol = bound(A, reach, v_max, ref, dt == torch.float16, wide)[inside]
+            assert not torch.isnan(err).any(), path
+            assert (err <= tol).all(), (path, float((err / tol).max()), (err / tol).flatten(1).amax(1).tolist()[:40])
+            assert (out[:cu[0]] == 77).all() and (out[cu[-1]:] == 77).all()
+            none = lse[inside].isinf()
+            assert torch.equal(l[inside].isinf() & (l[inside] < 0), none)
+            assert (out[inside][none] == 0).all()
+            e_u = score_error(reach, ref.shape[-1], wide)
+            assert ((l.double() - lse)[inside][~none].abs() <= (e_u + 2.0 ** -16 + lse.abs() * 2.0 ** -20)[inside][~none]).all()
+    qg.qift_debug_set_attention_path("auto")
     return out
 
 
@@ -361,10 +378,12 @@ def test_long_sequence_is_split():
     check(m, max_kv=64)  # a bound that is wrong changes how the work is split, not what it is
 
 
-def test_result_rotated_back():
-    m = make([1, 7, 40], [90, 30, 333], 8, 2, 128, 16, seed=4)
+@pytest.mark.parametrize("path,d", [("stream", 64), ("stream", 128), ("stream", 256), ("wide", 64), ("wide", 128)])
+def test_result_rotated_back(path, d):
+    m = make([1, 7, 40], [90, 30, 333], 8, 2, d, 16, seed=4)
+    qg.qift_debug_set_attention_path(path)
     x = call(m, out_dtype=torch.float32)
-    for block in (2, 16, 128):
+    for block in (2, 16, 32, 64, d):
         y = call(m, out_dtype=torch.float32, block=block)
         want = torch.from_numpy(hadamard_np(x.cpu().numpy(), block)).double()
         # the same sums before the rotation; its log2(block) stages and the last product round once each
@@ -375,9 +394,7 @@ def test_result_rotated_back():
 @pytest.mark.parametrize("gain", [1e-6, 1e3])
 def test_small_and_large_values(gain):
     m = make([1, 3], [300, 90], 8, 2, 128, 16, seed=6, gain=gain)
-    ref, _, A, e_u = reference(m)
-    out = call(m, out_dtype=torch.float32)
-    assert ((out.double() - ref).abs() <= bound(A, e_u, ref, False)).all()
+    check(m, dtypes=(torch.float32,))
 
 
 def test_values_of_very_different_size_and_zero_rows():
@@ -388,7 +405,9 @@ def test_values_of_very_different_size_and_zero_rows():
     m["cache"][1][0, :, 3] = 0.0                           # a key that is all zero
     check(m, dtypes=(torch.float32,))
     vs.zero_()
-    assert (call(m) == 0).all()
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        assert (call(m) == 0).all()
 
 
 def test_peaked_scores():
@@ -416,10 +435,12 @@ def test_pages_that_are_not_there():
 
 def test_contradicting_offsets_stay_inside():
     m = make([2, 2], [40, 50], 4, 2, 64, 16, seed=13)
-    for cu in ([0, 3, 2], [-5, 2, 4], [0, 2, 400], [4, 4, 4]):
-        out = torch.full((4, 4, 64), 7.0, device="cuda").half()
-        call(dict(m, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda")), out=out)
-    call(dict(m, kv_lens=torch.tensor([-3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")))
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        for cu in ([0, 3, 2], [-5, 2, 4], [0, 2, 400], [4, 4, 4]):
+            out = torch.full((4, 4, 64), 7.0, device="cuda").half()
+            call(dict(m, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda")), out=out)
+        call(dict(m, kv_lens=torch.tensor([-3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")))
     torch.cuda.synchronize()
 
 
@@ -436,7 +457,9 @@ def test_strided_queries():
     assert torch.equal(call(m), call(dict(m, q=wide[:, 2:10])))
 
 
-def test_a_pool_past_32_bits():
+@pytest.mark.parametrize("path", ["stream", "wide"])
+def test_a_pool_past_32_bits(path):
+    qg.qift_debug_set_attention_path(path)
     d, hk, size = 128, 8, 64
     pages = 2 ** 31 // (hk * size * d // 2) + 70            # over 2^31 bytes of codes
     m = make([1], [150], 8, hk, d, size, seed=16)
@@ -456,7 +479,9 @@ def test_a_pool_past_32_bits():
     assert torch.equal(k, v) and err.max() < 0.5 * x.float().norm(dim=-1).max() / 7
 
 
-def test_other_stream_and_captured_graphs():
+@pytest.mark.parametrize("path", ["stream", "wide"])
+def test_other_stream_and_captured_graphs(path):
+    qg.qift_debug_set_attention_path(path)
     m = make([1, 1], [9000, 4000], 8, 2, 128, 16, seed=17)
     want = call(m)
     s = torch.cuda.Stream()
@@ -488,7 +513,9 @@ def test_other_stream_and_captured_graphs():
 
 def test_same_call_twice_gives_the_same_bits():
     m = make([1] * 6 + [90], [3000, 40, 777, 5000, 1, 60, 4000], 32, 8, 128, 16, prefix=0, seed=18)
-    assert torch.equal(call(m), call(m))
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        assert torch.equal(call(m), call(m))
 
 
 def test_refusals_leave_the_result_alone():
@@ -550,6 +577,7 @@ def test_a_layer_prompt_then_single_tokens(window, sinks):
 
 def test_wait_that_runs_out_is_reported_and_the_context_survives():
     m = make([200], [300], 8, 2, 128, 16, seed=20)
+    qg.qift_debug_set_attention_path("wide")
     want = call(m)
     assert qg.qift_device_error() == (qg.QIFT_OK, 0)
     qg.qift_debug_set_wait_limit(20_000_000)               # about 10 ms a wait
@@ -561,3 +589,27 @@ def test_wait_that_runs_out_is_reported_and_the_context_survives():
     assert qg.qift_device_error() == (qg.QIFT_OK, 0)
     assert torch.equal(call(m), want)
     assert qg.qift_device_error() == (qg.QIFT_OK, 0)
+
+
+def test_the_kernel_for_many_rows_takes_head_dims_up_to_128():
+    m = make([40], [50], 2, 1, 256, 16, seed=22)
+    qg.qift_debug_set_attention_path("wide")
+    with pytest.raises(qg.QiftError) as e:
+        call(m)
+    assert e.value.status == qg.QIFT_ERR_UNSUPPORTED
+
+
+def test_the_choice_of_kernel_is_by_cost():
+    """A long prompt runs on the tensor memory kernel: its bits are those of the pinned call, and not those of the other."""
+    m = make([3000], [3000], 32, 8, 128, 16, seed=23)
+    auto = call(m)
+    got = {}
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        got[path] = call(m)
+    assert torch.equal(auto, got["wide"]) and not torch.equal(auto, got["stream"])
+    one = dict(make([1] * 3, [500, 60, 7], 32, 8, 128, 16, seed=24))
+    qg.qift_debug_set_attention_path("auto")
+    auto = call(one)
+    qg.qift_debug_set_attention_path("stream")
+    assert torch.equal(auto, call(one))

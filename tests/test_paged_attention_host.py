@@ -125,3 +125,16 @@ def test_binding_refuses_cpu_tensors():
         q.qift_gather_kv(*c, s, 64)
     with pytest.raises(ValueError):
         q.qift_paged_attention(x, None, 1, *c, torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+
+
+def test_attention_path_pin(L):
+    size = q.qift_paged_attention_workspace
+    assert L.qift_debug_set_attention_path(7) == BAD
+    q.qift_debug_set_attention_path("wide")
+    try:
+        assert size(1, 32, 8, 128, 1, 1, 16, 8192) > 0
+        with pytest.raises(ValueError):
+            size(1, 8, 2, 256, 1, 1, 16, 8192)                         # not for this head_dim
+    finally:
+        q.qift_debug_set_attention_path("auto")
+    assert size(1, 8, 2, 256, 1, 1, 16, 8192) > 0

@@ -67,6 +67,7 @@ def lib() -> C.CDLL:
         L.qift_debug_stall_next_gemm.argtypes = []
         L.qift_debug_stall_next_one_token.argtypes = []
         L.qift_debug_stall_next_attention.argtypes = []
+        L.qift_debug_set_attention_path.argtypes = [i32]
         L.qift_debug_set_linear_path.argtypes = [i32]
         L.qift_debug_set_pdl.argtypes = [i32]
         L.qift_debug_check_line.argtypes = [C.POINTER(i32)]
@@ -81,6 +82,7 @@ def lib() -> C.CDLL:
                      "qift_append_kv", "qift_gather_kv", "qift_paged_attention",
                      "qift_device_error", "qift_debug_set_wait_limit", "qift_debug_stall_next_gemm",
                      "qift_debug_stall_next_one_token", "qift_debug_stall_next_attention",
+                     "qift_debug_set_attention_path",
                      "qift_debug_set_linear_path", "qift_debug_set_pdl", "qift_debug_check_line"):
             getattr(L, name).restype = C.c_int
         _lib = L
@@ -602,6 +604,16 @@ def qift_debug_set_linear_path(path) -> None:
     "gemm_pair", "one_token")."""
     p = LINEAR_PATHS[path] if isinstance(path, str) else int(path)
     _check(lib().qift_debug_set_linear_path(p), "qift_debug_set_linear_path")
+
+
+ATTENTION_PATHS = {"auto": 0, "stream": 1, "wide": 2}
+
+
+def qift_debug_set_attention_path(path) -> None:
+    """Test hook: pin qift_paged_attention's kernel in this thread ("auto", "stream", "wide")."""
+    p = ATTENTION_PATHS[path] if isinstance(path, str) else int(path)
+    _check(lib().qift_debug_set_attention_path(p), "qift_debug_set_attention_path")
+    _workspace_bytes.cache_clear()  # the answer is the pinned kernel's
 
 
 def qift_debug_set_pdl(enable: bool) -> None:

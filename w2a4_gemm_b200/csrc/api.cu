@@ -516,6 +516,13 @@ qift_status qift_debug_stall_next_one_token(void) {
     return QIFT_OK;
 }
 
+qift_status qift_debug_set_attention_path(int32_t path) {
+    if (path != qift::kAttentionAuto && path != qift::kAttentionStream && path != qift::kAttentionWide)
+        return QIFT_ERR_INVALID_ARG;
+    qift::debug_set_attention_path(path);
+    return QIFT_OK;
+}
+
 qift_status qift_debug_stall_next_attention(void) {
     qift::debug_stall_next_attention();
     return QIFT_OK;

@@ -557,55 +557,76 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     finish_row<D>(a, acc, M, L, token, head, lane);
 }
 
-// Rows a kv head from which a row set goes to the kernel for many rows.
-constexpr int64_t kWideFrom = 64;
-
-// Rows of a block of the streaming kernel: 8 where no row set it takes has more.
-static int stream_rows(const AttentionArgs& a) {
-    const int64_t G = a.q_heads / a.kv_heads;
-    return a.max_q * G <= 8 && (!a.prefix_len || a.tokens * G <= 8 || (a.head_dim <= 128 && a.tokens * G >= kWideFrom))
-               ? 8
-               : 16;
+// How one kind of row sets (the prefix's, or the sequences' own) is cut into blocks.
+struct Cut {
+    int tiles, splits, chunk;
+    double us;  // what it takes, roughly
+};
+// `sets` row sets of `rows` rows and at most `keys` keys, on the streaming kernel (`per` rows a block) or the
+// one for many rows.
+// Streaming: a split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths, at most 4096.
+// Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by 8 kv heads
+// took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the bound on their
+// lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with one turn, 179
+// with two and 174 with four.
+// Many rows: one block an SM, split only where there are fewer row sets than SMs.
+static Cut cut(bool wide, int per, int64_t sets, int64_t rows, int64_t keys, bool equal, int head_dim) {
+    Cut c = {};
+    const int64_t step = wide ? kWideStep : kStep;
+    const int64_t least = 512 / step, most = wide || equal ? 1 << 20 : 4096 / step;
+    const int64_t steps = (keys + step - 1) / step + 1;
+    c.tiles = (int)((rows + per - 1) / per);
+    const int64_t blocks = sets * c.tiles;
+    int64_t n = wide ? 148 / blocks : (equal ? 1 : 2) * 592 / blocks;
+    n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
+    n = std::min<int64_t>(n, kMostSlots / 2);
+    c.chunk = (int)((steps + n - 1) / n);
+    c.splits = (int)((steps + c.chunk - 1) / c.chunk);
+    // Measured with head_dim 128: a streamed key takes 0.038 ns for a block of 16 rows and 0.024 for one of 8
+    // when the GPU is full, a block as much more as 300 keys, a launch 9 us; a step of 256 rows by 128 keys
+    // takes an SM 2.3 us, a launch 17.
+    const int64_t all = blocks * c.splits;
+    c.us = wide ? 17.0 + (double)((all + 147) / 148) * c.chunk * 2.3
+                : 9.0 + (double)all * ((double)c.chunk * kStep + 300.0) * (per == 8 ? 24e-6 : 38e-6) * head_dim / 128;
+    return c;
 }
 
+// Rows of a block of the streaming kernel.
+static int stream_rows(const AttentionArgs& a, const Deal& d) {
+    const int64_t G = a.q_heads / a.kv_heads;
+    return (d.own_wide || a.max_q * G <= 8) && (d.prefix_wide || !a.prefix_len || a.tokens * G <= 8) ? 8 : 16;
+}
+
+// Which kernel takes what: the one that takes less by the measure above.  A step of 256 rows costs the same
+// for fewer, so few rows stream: 64 sequences' single tokens of four query heads a kv head against a
+// prefix of 32000 keys took 52 us either way, 16 of them 27 us streamed and 53, 128 of them 85 and 57.
 static Deal deal_out(const AttentionArgs& a) {
-    const int G = a.q_heads / a.kv_heads;
-    const int64_t own_rows = (int64_t)a.max_q * G, shared_rows = a.tokens * G;
-    Deal d = {};
-    d.own_wide = a.head_dim <= 128 && own_rows >= kWideFrom;
-    d.prefix_wide = a.head_dim <= 128 && shared_rows >= kWideFrom;
-    // The streaming kernel.  A split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths,
-    // at most 4096.  Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by
-    // 8 kv heads took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the
-    // bound on their lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with
-    // one turn, 179 with two and 174 with four.
-    // The kernel for many rows has one block an SM; it is split only where there are fewer row sets than SMs.
+    const int64_t G = a.q_heads / a.kv_heads, own_rows = a.max_q * G, shared_rows = a.tokens * G;
     const bool equal = a.batch == 1 || a.window > 0;
-    auto split = [&](bool wide, int64_t blocks, int64_t keys, int turns, int* splits, int* chunk) {
-        const int64_t step = wide ? kWideStep : kStep;
-        const int64_t least = 512 / step, most = wide || equal ? 1 << 20 : 4096 / step;
-        const int64_t steps = (keys + step - 1) / step + 1;
-        int64_t n = wide ? 148 / blocks : turns * 592 / blocks;
-        n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
-        n = std::min<int64_t>(n, kMostSlots / 2);
-        *chunk = (int)((steps + n - 1) / n);
-        *splits = (int)((steps + *chunk - 1) / *chunk);
-    };
-    auto tiles_of = [&](bool wide, int64_t rows) {
-        const int per = wide ? kWideRows : stream_rows(a);
-        return (int)((rows + per - 1) / per);
-    };
     int64_t own = (int64_t)a.max_kv - a.prefix_len;
-    if (a.window) {
+    if (a.window)  // rows of the whole batch stand far apart: no such bound on what they see of the prefix
         own = std::min(own, (int64_t)a.window + a.max_q + a.sinks + 2 * kStep);
-        // rows of the whole batch stand at positions far apart: no bound on what they see of the prefix
-    }
     own = std::max<int64_t>(own, 1);
-    d.own_tiles = tiles_of(d.own_wide, own_rows);
-    split(d.own_wide, (int64_t)a.batch * a.kv_heads * d.own_tiles, own, equal ? 1 : 2, &d.own_splits, &d.own_chunk);
+    const int64_t own_sets = (int64_t)a.batch * a.kv_heads;
+    auto own_cut = [&](bool wide, int per) { return cut(wide, wide ? kWideRows : per, own_sets, own_rows, own, equal, a.head_dim); };
+    auto shared_cut = [&](bool wide, int per) {
+        return cut(wide, wide ? kWideRows : per, a.kv_heads, shared_rows, a.prefix_len, true, a.head_dim);
+    };
+    Deal d = {};
+    const int pin = debug_attention_path();
+    if (pin == kAttentionWide) {
+        d.own_wide = true;
+        d.prefix_wide = a.prefix_len > 0;
+    } else if (a.head_dim <= 128 && pin == kAttentionAuto) {
+        d.own_wide = own_rows > 16 && own_cut(true, 0).us < own_cut(false, 16).us;
+        d.prefix_wide = a.prefix_len && shared_rows > 16 && shared_cut(true, 0).us < shared_cut(false, 16).us;
+    }
+    const int per = stream_rows(a, d);
+    const Cut c = own_cut(d.own_wide, per);
+    d.own_tiles = c.tiles, d.own_splits = c.splits, d.own_chunk = c.chunk;
     if (a.prefix_len) {
-        d.prefix_tiles = tiles_of(d.prefix_wide, shared_rows);
-        split(d.prefix_wide, (int64_t)a.kv_heads * d.prefix_tiles, a.prefix_len, 1, &d.prefix_splits, &d.prefix_chunk);
+        const Cut p = shared_cut(d.prefix_wide, per);
+        d.prefix_tiles = p.tiles, d.prefix_splits = p.splits, d.prefix_chunk = p.chunk;
     }
     d.slots = a.prefix_len || d.own_splits > 1 ? d.prefix_splits + d.own_splits : 0;
     return d;
@@ -651,8 +672,8 @@ static cudaError_t launch_all(const AttentionArgs& a, const Deal& d, cudaStream_
         if (d.prefix_wide != wide) part.prefix_tiles = 0;
         if (d.own_wide != wide) part.own_tiles = 0;
         if (part.blocks(a.batch, a.kv_heads) == 0) continue;
-        const cudaError_t e = wide                  ? launch_wide(a, part, s)
-                              : stream_rows(a) == 8 ? launch_stream<D, 1>(a, part, s)
+        const cudaError_t e = wide                     ? launch_wide(a, part, s)
+                              : stream_rows(a, d) == 8 ? launch_stream<D, 1>(a, part, s)
                                                     : launch_stream<D, 2>(a, part, s);
         if (e != cudaSuccess) return e;
     }
@@ -661,7 +682,12 @@ static cudaError_t launch_all(const AttentionArgs& a, const Deal& d, cudaStream_
 
 }  // namespace attn
 
+static thread_local int g_attention_path = kAttentionAuto;
+void debug_set_attention_path(int path) { g_attention_path = path; }
+int debug_attention_path() { return g_attention_path; }
+
 bool attention_supported(const AttentionArgs& a) {
+    if (debug_attention_path() == kAttentionWide && a.head_dim > 128) return false;
     const attn::Deal d = attn::deal_out(a);
     return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads <= 0x7fffffff;
 }

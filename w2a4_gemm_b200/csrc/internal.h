@@ -163,6 +163,10 @@ struct AttentionArgs {
 bool attention_supported(const AttentionArgs& a);
 int64_t attention_workspace_bytes(const AttentionArgs& a);
 cudaError_t launch_attention(AttentionArgs a, cudaStream_t s);
+// Test hook: pins the attention kernel of every row set (per host thread).
+enum AttentionPath { kAttentionAuto = 0, kAttentionStream = 1, kAttentionWide = 2 };
+void debug_set_attention_path(int path);
+int debug_attention_path();
 void debug_set_attention_wait_limit(long long cycles);
 void debug_stall_next_attention();
 cudaError_t read_and_clear_attention_error(int* word);
