@@ -347,7 +347,7 @@ qift_status qift_append_kv(const void* q, int64_t q_stride, const void* k, int64
     a.q_stride = q_stride;
     a.k_stride = k_stride;
     a.v_stride = v_stride;
-    a.rows = tokens * ((int64_t)q_heads + 2 * kv_heads);
+    a.tokens = tokens;
     a.q_heads = q_heads;
     a.kv_heads = kv_heads;
     a.rope = rope;

@@ -102,12 +102,12 @@ bool linear_w4_supported(int64_t tokens, int64_t n_in);
 cudaError_t launch_linear_w4(const int8_t* q, const float* s_a, const uint32_t* codes, const float* s_w,
                              int64_t tokens, int64_t n_out, int64_t n_in, void* y, bool f16, cudaStream_t s);
 
-// Paged KV4 cache (qift_append_kv, qift_gather_kv).  rows = tokens * heads handled, one row of head_dim
-// values each; the launchers fill in `norm`.
+// Paged KV4 cache (qift_append_kv, qift_gather_kv; GatherArgs::rows: tokens times heads of keys and values).
+// The launchers fill in `norm`.
 struct AppendArgs {
     const __half *q, *k, *v;
     int64_t q_stride, k_stride, v_stride;  // elements between tokens
-    int64_t rows;
+    int64_t tokens;
     int q_heads, kv_heads;                 // q_heads 0: no queries
     const float* rope;                     // [rope_len][rope_dim], or null: no position rotation
     int64_t rope_len;
@@ -120,6 +120,7 @@ struct AppendArgs {
     float *k_scales, *v_scales;
     int64_t n_pages;
     int log_page;
+    int slots_per_token, heads_per_slot, tokens_per_block;  // filled in by the launcher
 };
 struct GatherArgs {
     const uint8_t *k_cache, *v_cache;
