@@ -477,6 +477,57 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     }
 }
 
+// The same for rows of up to 32 slots, a warp a row: a lane holds a slot's weight.  (4096 rows of 10 slots, a
+// block each: 17.8 us.)
+template <int D>
+__global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, const int slots) {
+    constexpr int E = D / 32;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int head = (int)(row % a.q_heads);
+    row /= a.q_heads;
+    const int i = (int)(row % a.max_q);
+    const int64_t b = row / a.max_q;
+    if (b >= a.batch) return;
+    const Sequence s = sequence(a, (int)b);
+    if (i >= s.q_len) return;
+    const int64_t token = s.first + i;
+    const Parts p = parts(a, slots);
+    const int64_t at = (token * a.q_heads + head) * slots;
+    const float2 ml = lane < slots ? p.ml[at + lane] : make_float2(kNone, 0.0f);
+    float M = ml.x;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    const float f = ml.y > 0.0f ? ex2(ml.x - M) : 0.0f;
+    float L = f * ml.y, acc[E];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int k0 = 0; k0 < slots; k0 += 4) {
+        float w[4], v[4][E];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            w[u] = __shfl_sync(0xffffffffu, f, (k0 + u) & 31);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
+            if (k0 + u < slots && w[u] > 0.0f) {  // an empty slot's O was never written
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    *reinterpret_cast<float2*>(&v[u][e]) =
+                        *reinterpret_cast<const float2*>(p.o + (at + k0 + u) * D + lane * E + e);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(k0 + u < slots ? w[u] : 0.0f, v[u][e], acc[e]);
+    }
+    finish_row<D>(a, acc, M, L, token, head, lane);
+}
+
 // Joins the partial results of a row, one block a row; rows are dealt out as (sequence, token, head).
 // All (M, L) are read at once and become weights in shared memory, then each warp sums every
 // kJoinWarps-th slot with four loads in flight: what it costs is the chain of loads, so the chain is
@@ -653,16 +704,18 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
 template <int D>
 static cudaError_t launch_join(const AttentionArgs& a, int slots, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.batch * a.max_q * a.q_heads));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = slots * sizeof(float);
+    const int64_t rows = (int64_t)a.batch * a.max_q * a.q_heads;
+    const bool few = slots <= 32 && rows >= 148 * 2;  // a warp a row only where that fills the GPU
+    cfg.gridDim = dim3((unsigned)(few ? (rows + 7) / 8 : rows));
+    cfg.blockDim = dim3(few ? 256 : 32 * kJoinWarps);
+    cfg.dynamicSmemBytes = few ? 0 : slots * sizeof(float);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a, slots);
+    return cudaLaunchKernelEx(&cfg, few ? join_few_kernel<D> : join_kernel<D>, a, slots);
 }
 
 template <int D>
