@@ -285,7 +285,8 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *               NULL where that is 0.  Two calls that may run at once, or captured graphs that may,
  *               need one each.
  * Scores, the softmax's sums and the weighted sum are fp32; the weights, times their value's scale,
- * are rounded once to binary16 (11 bits, 2^-12 of each) for the tensor cores.
+ * are rounded once to binary16 (2^-11 of each at most) for the tensor cores.  Scales in the cache lie in
+ * [0, 65504/7], as qift_append_kv writes them.
  * qift_paged_attention_workspace returns the bytes for a call of these sizes, or -1 if qift_paged_attention
  * would refuse them.  head_dim, page_size: as above.  (max_pages * page_size + prefix_len) <= 2^30.
  */

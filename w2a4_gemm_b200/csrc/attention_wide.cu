@@ -5,18 +5,15 @@
 // Inference" names KV4.  The formula is attention.cu's.  A block takes two tiles of 128 rows against
 // the same keys, 128 at a time:
 //   S = Q K^T   (binary16 x binary16 -> fp32 in tensor memory)
-//   p_j = 2^(k S_j + e - ref), rounded to binary16 into tensor memory over S
+//   p_j = 2^(scale s_j S_j - ref) t_j, rounded to binary16 into tensor memory over S
 //   O += P V    (P from tensor memory, O stays there)
-// K and V come from the paged 4-bit cache: bulk copies bring the codes, and four warps
-// write the values in binary16 in the layout the tensor core reads: K rows of keys, V transposed (rows
-// of values, so that both operands are contiguous along the sum), 128-byte swizzled.  The order of
-// values inside each group of eight is that in which a word's nibbles come out; Q is laid out alike.
-// A value is code * m / 2^e, m = 7 s the row's largest magnitude (a binary16 value, so the product is
-// the only rounding: 2^-12 of the value, that of the binary16 values qift_gather_kv returns) and 2^e the
-// power of two of the largest m of 32 keys; 2^e of K (with 1/7 and the softmax scale) is the factor k, that
-// of V the e above, so small values lose nothing.  With the exact codes as operands and the scales
-// applied to S and P, each row's thread reads 128 pairs of scales a step from shared memory: that read
-// took two thirds of the load pipe, and the prompt of 8192 tokens 951 us.
+// K and V come from the paged 4-bit cache: bulk copies bring the codes, and four warps write them as exact
+// whole numbers in binary16 in the layout the tensor core reads: K rows of keys, V transposed (rows of
+// values, so that both operands are contiguous along the sum), 128-byte swizzled.  The scales are applied
+// in fp32 to S and to the weights, so the one rounding is that of p.  (Folded into the binary16 operands
+// instead, scales cost nothing in the softmax and the prompt of 8192 tokens took 598 us for 614, but the
+// result's error was 5.5e-4 for 2.9e-4.)  The order of values inside each group of eight is that in which a
+// word's nibbles come out; Q is laid out alike.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
 //   warps 8-11       unpack K, V; copy the scales
@@ -24,8 +21,15 @@
 //   warp 14          copies codes and scales from the cache (15 fills the register group)
 // One tile's products run under the other's softmax.
 //
-// A row's reference is raised (and O scaled down) only when the weights of a step might not fit
-// binary16: the test is their sum, which is needed anyway.
+// A row's reference is raised (and O scaled down) only when the weights of a half step might not fit
+// binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j.
+//
+// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 614 us, 56% of the
+// measured bf16 matrix rate over the visible half): a step of 256 rows by 128 keys takes about 4000 cycles.
+// S in halves of 64 keys costs the tensor core about 90 cycles a product, half of its rate, since Q is read
+// from shared memory for each; P V 64; together some 3300.  The exponentials of 256 x 128 weights take the
+// special-function unit 2048.  Exponentials on the fp32 pipe (a polynomial for a quarter to a half of the
+// weights) made it slower (690-740 us): the softmax waits for latency, not for that unit.
 //
 // Every wait is bounded: one that runs out sets a shared abort flag and the device error word, every
 // role leaves its loop, the products in flight are waited for and tensor memory is freed.
@@ -78,7 +82,7 @@ struct Shape {
     // Codes and scales as they come from the cache: keys one behind the other, values in eights of keys 16
     // bytes apart, so that the transposing reads meet no bank twice.
     static constexpr int V_STRIDE = 8 * ROW + 16;
-    static constexpr int KC_AT = SC_AT + RING * 36 + BN * 4 + 16 - (RING * 36) % 16, VC_AT = KC_AT + BN * ROW;
+    static constexpr int KC_AT = SC_AT + RING * (BN * 8 + 16 + 4), VC_AT = KC_AT + BN * ROW;
     static constexpr int KS_AT = VC_AT + (BN / 8) * V_STRIDE, VS_AT = KS_AT + BN * 4;
     static constexpr int BAR_AT = VS_AT + BN * 4;
     static constexpr int SMEM = BAR_AT + 320;
@@ -92,7 +96,6 @@ struct Shape {
 struct Bars {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t scales[RING];
-    uint64_t ratios;
     uint64_t q_full[TILES];
     uint64_t kc_full, kc_empty, vc_full, vc_empty;  // codes and scales as they come from the cache
     uint64_t s_full[TILES][2], p_full[TILES][2], o_done[TILES][2];  // by halves of a step
@@ -193,17 +196,8 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t mulh2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-// The largest magnitude of a row of the cache from its scale s = m / 7: 7 s rounds to m, a binary16
-// value.  What no row can have (a scale that was never written) counts as 0.
-__device__ __forceinline__ float scale7(float s) {
-    return s >= 0.0f && s <= 9358.0f ? __half2float(__float2half_rn(7.0f * s)) : 0.0f;
-}
-__device__ __forceinline__ int exponent(float m) { return max((int)(__float_as_uint(m) >> 23) - 127, -28); }
-__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// A scale of the cache.  What none can be (a row that was never written) counts as 0.
+__device__ __forceinline__ float scale_of(float s) { return s >= 0.0f && s <= 9358.0f ? s : 0.0f; }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&x)[16]) {
     asm volatile(
@@ -230,14 +224,16 @@ struct View {
     }
 };
 
-// Weights of half a step: S of this thread's row from tensor memory, p = 2^(k S + e - ref) in binary16
-// pairs, k and e by chunk of 32 keys; `first` is the half's first key in the view.  total: sum of p; the
-// result: sum of 2^(k S - ref).
+// Weights of half a step: S of this thread's row from tensor memory, p = 2^(k_j S_j - ref) t_j in binary16
+// pairs, k_j and t_j in shared memory; `first` is the half's first key in the view, `most` the largest t_j of
+// each chunk of 32 keys.  total: at least the sum of p; the result: sum of 2^(k_j S_j - ref).
 template <bool MASK>
-__device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[2], const float (&e)[2], float ref,
-                                       const View& view, int first, uint32_t (&p)[BH / 2], float& total) {
+__device__ __forceinline__ float weigh(uint32_t taddr, const ulonglong2* ks, const ulonglong2* ts, float most0,
+                                       float most1, float ref, const View& view, int first, uint32_t (&p)[BH / 2],
+                                       float& total) {
     uint32_t in[2][32];
     tc::tmem_ld_32x32b_x32(taddr, in[0]);
+    const uint64_t off = pack2(-ref, -ref);
     float part = 0.0f;
     total = 0.0f;
 #pragma unroll
@@ -245,34 +241,39 @@ __device__ __forceinline__ float weigh(uint32_t taddr, const float (&k)[2], cons
         uint32_t(&x)[32] = in[c & 1];
         tmem_ld_wait_for(x);
         if (c + 1 < BH / 32) tc::tmem_ld_32x32b_x32(taddr + 32 * (c + 1), in[(c + 1) & 1]);
-        const uint64_t k2 = pack2(k[c], k[c]), off = pack2(e[c] - ref, e[c] - ref);
         uint64_t sum = pack2(0.0f, 0.0f);
         const uint32_t seen = MASK ? view.bits(first + c * 32) : 0u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float u0, u1;
-            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), k2, off), u0, u1);
-            if (MASK) {
-                u0 = seen & (1u << (2 * i)) ? u0 : -INFINITY;
-                u1 = seen & (2u << (2 * i)) ? u1 : -INFINITY;
+        for (int i = 0; i < 16; i += 2) {
+            const ulonglong2 k4 = ks[c * 8 + i / 2], t4 = ts[c * 8 + i / 2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int j = i + q;
+                float u0, u1, p0, p1;
+                unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), q ? k4.y : k4.x, off), u0, u1);
+                if (MASK) {
+                    u0 = seen & (1u << (2 * j)) ? u0 : -INFINITY;
+                    u1 = seen & (2u << (2 * j)) ? u1 : -INFINITY;
+                }
+                const uint64_t w = pack2(ex2(u0), ex2(u1));
+                sum = add2(sum, w);
+                unpack2(mul2(w, q ? t4.y : t4.x), p0, p1);
+                const __half2 h = __floats2half2_rn(p0, p1);
+                p[c * 16 + j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            const float w0 = ex2(u0), w1 = ex2(u1);
-            sum = add2(sum, pack2(w0, w1));
-            const __half2 h = __floats2half2_rn(w0, w1);
-            p[c * 16 + i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         float s0, s1;
         unpack2(sum, s0, s1);
         s0 += s1;
-        total += s0;
-        part = __fmaf_rn(s0, ex2(-e[c]), part);
+        total = __fmaf_rn(s0, c ? most1 : most0, total);
+        part += s0;
     }
     return part;
 }
 
-// The largest k S + e of half a step.
-__device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[2], const float (&e)[2], const View& view,
-                                         int first, bool mask) {
+// The largest k_j S_j + log2 t_j of half a step.
+__device__ __forceinline__ float largest(uint32_t taddr, const float* ks, const float* ts, const View& view, int first,
+                                         bool mask) {
     float top = -INFINITY;
 #pragma unroll
     for (int c = 0; c < BH / 32; ++c) {
@@ -282,7 +283,7 @@ __device__ __forceinline__ float largest(uint32_t taddr, const float (&k)[2], co
         const uint32_t seen = mask ? view.bits(first + c * 32) : 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float u = __fmaf_rn(__uint_as_float(x[i]), k[c], e[c]);
+            const float u = __fmaf_rn(__uint_as_float(x[i]), ks[c * 32 + i], fmaxf(lg2(ts[c * 32 + i]), -28.0f));
             if (seen & (1u << i)) top = fmaxf(top, u);
         }
     }
@@ -296,10 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];  // swizzled operands
     Bars& bar = *reinterpret_cast<Bars*>(smem + S::BAR_AT);
     const uint32_t base32 = tc::smem_u32(smem);
-    float4* factor_k = reinterpret_cast<float4*>(smem + S::SC_AT);      // [RING] k of the step's four 32s of keys
-    float4* power_v = factor_k + RING;                                   // [RING] e
-    uint32_t* gone = reinterpret_cast<uint32_t*>(power_v + RING);        // [RING] 16s of keys that are not there
-    __half* ratio_v = reinterpret_cast<__half*>(smem + S::KC_AT - BN * 4);  // [2][BN]
+    float* key_scales = reinterpret_cast<float*>(smem + S::SC_AT);       // [RING][BN], times the softmax scale
+    float* value_scales = key_scales + RING * BN;                        // [RING][BN]
+    float4* most = reinterpret_cast<float4*>(value_scales + RING * BN);  // [RING] largest t of the step's four 32s of keys
+    uint32_t* gone = reinterpret_cast<uint32_t*>(most + RING);           // [RING] 16s of keys that are not there
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in all lanes
     const int G = a.q_heads / a.kv_heads;
@@ -339,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar.pmin[i] = bar.least[i] = 0x7fffffff;
             bar.pmax[i] = -1;
         }
-        tc::mbar_init(&bar.ratios, kUnpackThreads);
         tc::mbar_init(&bar.kc_full, 1);
         tc::mbar_init(&bar.vc_full, 1);
         tc::mbar_init(&bar.kc_empty, kUnpackThreads);
@@ -429,25 +429,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ring = i % RING;
             ok = __all_sync(0xffffffffu, wait(&bar.scales[ring], (i / RING) & 1, &bar.abort, limit));
             if (!ok) break;
-            const float4 k4 = factor_k[ring], e4 = power_v[ring];
+            const float4 m4 = most[ring];
+            const float *ks = key_scales + ring * BN, *ts = value_scales + ring * BN;
             view.j0 = base + block_of(i) * BN;
             view.gone = gone[ring];
             const bool mask = !(view.j0 + BN - 1 <= t_least && view.j0 + BN <= base + range.limit && view.gone == 0 &&
                                 (!a.window || view.j0 > t_pmax - a.window || view.j0 + BN <= a.sinks));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const float k[2] = {half ? k4.z : k4.x, half ? k4.w : k4.y};
-                const float e[2] = {half ? e4.z : e4.x, half ? e4.w : e4.y};
+                const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(ks + half * BH);
+                const ulonglong2* t2 = reinterpret_cast<const ulonglong2*>(ts + half * BH);
+                const float m0 = half ? m4.z : m4.x, m1 = half ? m4.w : m4.y;
                 const uint32_t t_h = t_s + half * BH;
                 ok = __all_sync(0xffffffffu, wait(&bar.s_full[tile][half], i & 1, &bar.abort, limit));
                 if (!ok) break;
                 tc::tc_fence_after();
                 uint32_t p[BH / 2];
                 float total;
-                float part = mask ? weigh<true>(t_h, k, e, ref, view, half * BH, p, total)
-                                  : weigh<false>(t_h, k, e, ref, view, half * BH, p, total);
+                float part = mask ? weigh<true>(t_h, k2, t2, m0, m1, ref, view, half * BH, p, total)
+                                  : weigh<false>(t_h, k2, t2, m0, m1, ref, view, half * BH, p, total);
                 if (!__all_sync(0xffffffffu, total <= kMostWeight)) {
-                    const float to = fmaxf(ref, largest(t_h, k, e, view, half * BH, mask) - kLift);
+                    const float to = fmaxf(ref, largest(t_h, ks + half * BH, ts + half * BH, view, half * BH, mask) - kLift);
                     const float down = ex2(ref - to);
                     ref = to;
                     sum *= down;
@@ -466,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc::tmem_st_wait();
                     }
-                    part = mask ? weigh<true>(t_h, k, e, ref, view, half * BH, p, total)
-                                : weigh<false>(t_h, k, e, ref, view, half * BH, p, total);
+                    part = mask ? weigh<true>(t_h, k2, t2, m0, m1, ref, view, half * BH, p, total)
+                                : weigh<false>(t_h, k2, t2, m0, m1, ref, view, half * BH, p, total);
                 }
                 sum += part;
                 tc::tmem_st_32x32b_x32(t_h, p);  // over the S that is read
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tc_fence_after();
             const bool finish = deal.slots == 0;
             const int block = finish ? a.block : 0;
-            const float by = (finish ? (sum > 0.0f ? __fdiv_rn(1.0f, 7.0f * sum) : 0.0f) : 1.0f / 7.0f) *
+            const float by = (finish ? (sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f) : 1.0f) *
                              (block ? a.norm : 1.0f);
             int64_t at = token >= 0 ? token * a.q_heads + head : -1;
             if (finish) {
@@ -593,22 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ks = is ? reinterpret_cast<const float*>(smem + S::KS_AT)[u] : 0.0f;
             const float vs = is ? reinterpret_cast<const float*>(smem + S::VS_AT)[u] : 0.0f;
             // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free.
-            // This warp's 32 keys are a chunk: m = 7 s by a power of two, that of the largest.
-            const float mk = scale7(ks), mv = scale7(vs);
-            float most_k = mk, most_v = mv;
+            const float t = scale_of(vs);
+            key_scales[ring * BN + u] = scale_of(ks) * a.scale_log2;
+            value_scales[ring * BN + u] = t;
+            float top = t;  // of this warp's 32 keys
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) {
-                most_k = fmaxf(most_k, __shfl_xor_sync(0xffffffffu, most_k, m));
-                most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, m));
-            }
-            const int ek = exponent(most_k), ev = exponent(most_v);
-            const uint32_t rk = __half_as_ushort(__float2half_rn(mk * power(-ek)));
-            ratio_v[(i & 1) * BN + u] = __float2half_rn(mv * power(-ev));  // that of step i - 2 is read: `ratios` of step i - 1
-            tc::mbar_arrive(&bar.ratios);
-            if (lane == 0) {
-                reinterpret_cast<float*>(factor_k + ring)[w] = power(ek) * (a.scale_log2 * (1.0f / 7.0f));
-                reinterpret_cast<float*>(power_v + ring)[w] = (float)ev;
-            }
+            for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            if (lane == 0) reinterpret_cast<float*>(most + ring)[w] = top;
             tc::mbar_arrive(&bar.scales[ring]);
             const uint32_t k_to = base32 + S::K_AT + st * S::K_BYTES;
             // 16-byte piece cc of key kk of this warp's 32 holds groups 4 cc .. 4 cc + 3 of eight values.  Lanes read
@@ -619,25 +612,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint4 x4 = *reinterpret_cast<const uint4*>(smem + S::KC_AT + (w * 32 + kk) * S::ROW + cc * 16);
                 const bool swap = (cc >> 1) & 1;
                 const uint32_t words[4] = {swap ? x4.z : x4.x, swap ? x4.w : x4.y, swap ? x4.x : x4.z, swap ? x4.y : x4.w};
-                const uint32_t r1 = __shfl_sync(0xffffffffu, rk, kk), r2 = r1 | (r1 << 16);
                 const uint32_t to = k_to + (w * 32 + kk) * 128 + (cc >> 1) * (BN * 128);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = (cc & 1) * 4 + (swap ? e ^ 2 : e);
                     const uint32_t x = words[e], y = words[e] >> 8;
-                    sts128(to + ((c ^ (kk & 7)) << 4), mulh2(nib.lo(x), r2), mulh2(nib.hi(x), r2), mulh2(nib.lo(y), r2),
-                           mulh2(nib.hi(y), r2));
+                    sts128(to + ((c ^ (kk & 7)) << 4), nib.lo(x), nib.hi(x), nib.lo(y), nib.hi(y));
                 }
             }
             tc::mbar_arrive(&bar.kc_empty);
             tc::mbar_arrive(&bar.k_full[st]);
-            if (!__all_sync(0xffffffffu, wait(&bar.vc_full, i & 1, &bar.abort, limit) &&
-                                             wait(&bar.ratios, i & 1, &bar.abort, limit)))
-                break;
+            if (!__all_sync(0xffffffffu, wait(&bar.vc_full, i & 1, &bar.abort, limit))) break;
             if (i >= STAGES &&
                 !__all_sync(0xffffffffu, wait(&bar.v_empty[st], ((i - STAGES) / STAGES) & 1, &bar.abort, limit)))
                 break;
-            const uint4 rv4 = *reinterpret_cast<const uint4*>(ratio_v + (i & 1) * BN + v_kg * 8);
             uint32_t vq[8][S::VB / 4];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -649,7 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vq[j][0] = *reinterpret_cast<const uint32_t*>(from);
                 }
             }
-            const uint32_t rv[4] = {rv4.x, rv4.y, rv4.z, rv4.w};
             const uint32_t v_to = base32 + S::V_AT + st * S::V_BYTES + (v_kg >> 3) * (D * 128);
 #pragma unroll
             for (int wd = 0; wd < S::VB / 4; ++wd)
@@ -663,10 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 2; ++e) {
                         const int d8 = 4 * hf + 2 * e;  // value's place among the word's eight
                         const uint32_t to = v_to + (v_dc * (2 * S::VB) + wd * 8 + d8) * 128;
-                        sts128(to + (((v_kg & 7) ^ d8) << 4), mulh2(nib.lo(x[0]), rv[0]), mulh2(nib.lo(x[1]), rv[1]),
-                               mulh2(nib.lo(x[2]), rv[2]), mulh2(nib.lo(x[3]), rv[3]));
-                        sts128(to + 128 + (((v_kg & 7) ^ (d8 + 1)) << 4), mulh2(nib.hi(x[0]), rv[0]),
-                               mulh2(nib.hi(x[1]), rv[1]), mulh2(nib.hi(x[2]), rv[2]), mulh2(nib.hi(x[3]), rv[3]));
+                        sts128(to + (((v_kg & 7) ^ d8) << 4), nib.lo(x[0]), nib.lo(x[1]),
+                               nib.lo(x[2]), nib.lo(x[3]));
+                        sts128(to + 128 + (((v_kg & 7) ^ (d8 + 1)) << 4), nib.hi(x[0]),
+                               nib.hi(x[1]), nib.hi(x[2]), nib.hi(x[3]));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[k] >>= 8;
                     }
