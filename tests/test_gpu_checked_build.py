@@ -44,3 +44,18 @@ def test_checked_library_reports_itself():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=dict(os.environ, QIFT_LIB_PATH=lib),
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "ok" in r.stdout, (r.stdout + r.stderr)[-2000:]
+
+
+def test_paged_cache_suite_under_bounds_checks():
+    # Reads and writes of the paged cache go where a page table and slots on the device say: every place that a
+    # kernel computes from them is tested against the pool's extent.
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    lib = build.build(check=True)
+    env = dict(os.environ, QIFT_LIB_PATH=lib)
+    cmd = [sys.executable, "-m", "pytest", os.path.join(ROOT, "tests", "test_gpu_paged_attention.py"), "-m", "gpu", "-x",
+           "-q", "-k", "not runs_out", "-p", "no:cacheprovider"]
+    r = subprocess.run(cmd, cwd=ROOT, env=env, capture_output=True, text=True, timeout=1800)
+    tail = (r.stdout + r.stderr)[-3000:]
+    assert r.returncode == 0, tail
+    assert " passed" in r.stdout, tail

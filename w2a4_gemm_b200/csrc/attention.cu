@@ -45,7 +45,7 @@ struct Shape {
     static constexpr int OPAD = D + 4;
     static constexpr int ring_bytes() { return kWarps * STAGES * STAGE; }
     static constexpr int join_bytes(int nr) { return kWarps * 8 * nr * (OPAD + 2) * 4; }
-    static constexpr int smem(int nr) { return std::max(ring_bytes(), join_bytes(nr)); }
+    static constexpr int smem(int nr) { return std::max(ring_bytes(), join_bytes(nr)) + 128; }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -97,7 +97,8 @@ template <int D, int NR>
 __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stream_kernel(const AttentionArgs a, const Deal deal) {
     using S = Shape<D>;
     constexpr int R = 8 * NR;
-    extern __shared__ __align__(128) uint8_t smem[];  // rows of codes are swizzled by address bits 5 and 6
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* smem = aligned<128>(raw);  // rows of codes are swizzled by address bits 5 and 6
     __shared__ int64_t row_token[R];
     __shared__ int row_pos[R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;

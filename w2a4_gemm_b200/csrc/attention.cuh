@@ -21,6 +21,14 @@ namespace qift {
 namespace attn {
 
 constexpr int kMaxKeys = 1 << 30;  // of a sequence, so that positions plus a block stay in 32 bits
+// The first byte of dynamic shared memory at a multiple of ALIGN (which the declaration's own alignment does
+// not ensure in every build); the launch asks for ALIGN bytes more.
+template <int ALIGN>
+__device__ __forceinline__ uint8_t* aligned(uint8_t* raw) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(raw));
+    return raw + ((ALIGN - (at & (ALIGN - 1))) & (ALIGN - 1));
+}
+
 constexpr float kNone = -1e30f;  // finite, so that the difference of two of them is a number
 
 __device__ __forceinline__ float ex2(float x) {

@@ -85,7 +85,7 @@ struct Shape {
     static constexpr int KC_AT = SC_AT + RING * (BN * 8 + 16 + 4), VC_AT = KC_AT + BN * ROW;
     static constexpr int KS_AT = VC_AT + (BN / 8) * V_STRIDE, VS_AT = KS_AT + BN * 4;
     static constexpr int BAR_AT = VS_AT + BN * 4;
-    static constexpr int SMEM = BAR_AT + 320;
+    static constexpr int SMEM = BAR_AT + 320 + 1024;
     static_assert(KC_AT % 16 == 0 && VC_AT % 16 == 0 && KS_AT % 16 == 0 && BAR_AT % 16 == 0, "alignment");
     static constexpr int OPAD = D + 4;
     static_assert(TILES * BM * OPAD * 4 <= BAR_AT, "finished rows lie over the operands");
@@ -294,7 +294,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_kernel(const AttentionArgs a, const Deal deal, long long limit, int stall) {
     using S = Shape<D>;
-    extern __shared__ __align__(1024) uint8_t smem[];  // swizzled operands
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* smem = aligned<1024>(raw);  // swizzled operands
     Bars& bar = *reinterpret_cast<Bars*>(smem + S::BAR_AT);
     const uint32_t base32 = tc::smem_u32(smem);
     float* key_scales = reinterpret_cast<float*>(smem + S::SC_AT);       // [RING][BN], times the softmax scale
