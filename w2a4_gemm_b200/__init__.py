@@ -445,7 +445,7 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
         if hq == 0:
             raise ValueError("q must have at least one head")
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=torch.float16, device=k.device)
+            q_out = q.new_empty((T, hq, d))
             out_at = q_out.data_ptr()
         else:
             out_at = _is(q_out, "q_out", torch.float16, (T, hq, d), index)
@@ -465,8 +465,8 @@ def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch
     (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() else 0
     slots_at = _is(slots, "slots", torch.int64, (T,), index)
-    k = torch.empty((T, kv_heads, d), dtype=torch.float16, device=slots.device)
-    v = torch.empty((T, kv_heads, d), dtype=torch.float16, device=slots.device)
+    k = k_scales.new_empty((T, kv_heads, d), dtype=torch.float16)
+    v = torch.empty_like(k)
     _check(_launch(index, stream, lib().qift_gather_kv, kc, ks, vc, vs, pages, size, kv_heads, d, slots_at, T, block,
                    k.data_ptr(), v.data_ptr()), "qift_gather_kv")
     return k, v
@@ -496,9 +496,10 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     shape = q.shape
     T, hq = shape[0], shape[1]
     q_at, q_row = _heads(q, "q", (T, hq, d), index)
-    _2d(_cuda(page_table, "page_table", torch.int32), "page_table")
-    B, max_pages = page_table.shape
-    table_at = _is(page_table, "page_table", torch.int32, (B, max_pages), index)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [batch, max_pages] tensor")
+    B, max_pages = table_shape = page_table.shape
+    table_at = _is(page_table, "page_table", torch.int32, table_shape, index)
     lens_at = _is(kv_lens, "kv_lens", torch.int32, (B,), index)
     cu_at = prefix_at = lse_at = None
     if cu_q is not None:
@@ -521,13 +522,13 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
         ws_at, ws_bytes = _is(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
     elif need > 0:
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = k_cache.new_empty(need)
         else:  # freed, and used again, in the order of the stream that runs the kernels
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                workspace = k_cache.new_empty(need)
         ws_at, ws_bytes = workspace.data_ptr(), need
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+        out = torch.empty_like(q) if out_dtype is torch.float16 and q.is_contiguous() else q.new_empty(shape, dtype=out_dtype)
         out_at = out.data_ptr()
     else:
         out_at = _is(out, "out", out_dtype, shape, index)

@@ -386,7 +386,7 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
     a.v_cache = v_cache;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
-    a.rows = tokens * 2 * kv_heads;
+    a.rows = tokens * kv_heads;
     a.n_pages = n_pages;
     a.log_page = log2_of(page_size);
     a.kv_heads = kv_heads;

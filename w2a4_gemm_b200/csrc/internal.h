@@ -102,7 +102,7 @@ bool linear_w4_supported(int64_t tokens, int64_t n_in);
 cudaError_t launch_linear_w4(const int8_t* q, const float* s_a, const uint32_t* codes, const float* s_w,
                              int64_t tokens, int64_t n_out, int64_t n_in, void* y, bool f16, cudaStream_t s);
 
-// Paged KV4 cache (qift_append_kv, qift_gather_kv; GatherArgs::rows: tokens times heads of keys and values).
+// Paged KV4 cache (qift_append_kv, qift_gather_kv; GatherArgs::rows: tokens times heads).
 // The launchers fill in `norm`.
 struct AppendArgs {
     const __half *q, *k, *v;

@@ -105,7 +105,8 @@ __device__ __forceinline__ void rope8(float* v, const __half* row, int e, const 
     }
 }
 
-// WHOLE: the whole row is rotated, halves paired; the pairs and their cosines and sines are this lane's.
+// WHOLE: the usual call, known to the compiler: the whole row is rotated by its position, halves paired (the pairs
+// and their cosines and sines are this lane's), and by a Hadamard block of its own length.
 template <int D, bool WHOLE>
 __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs a) {
     constexpr int LANES = D / 16;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs 
                 rope8(v + 8, row, D / 2 + 8 * ts, tab, a.rope_dim, a.interleaved != 0);
             }
         }
-        row_hadamard16<D>(v, ts, a.block, a.norm);
+        row_hadamard16<D>(v, ts, WHOLE ? D : a.block, a.norm);
         uint4 packed[2];
         __half2* h2 = reinterpret_cast<__half2*>(packed);
         __half2 top = __float2half2_rn(0.0f);
@@ -196,7 +197,8 @@ __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs 
 }
 
 // Rows of the cache as fp16 values, rotated back: the row-wise inverse of the above.  Rows of slots
-// outside the cache are zeros.
+// outside the cache are zeros.  A lane's key and value rows are loaded together (a row each: 37 us for 8192
+// tokens of 32 heads, waiting for one load after the other).
 template <int D>
 __global__ void __launch_bounds__(kKvThreads) gather_kv_kernel(const GatherArgs a) {
     constexpr int LANES = D / 16;
@@ -204,40 +206,45 @@ __global__ void __launch_bounds__(kKvThreads) gather_kv_kernel(const GatherArgs 
     griddep_launch_dependents();
     const int ts = threadIdx.x % LANES;
     const uint32_t row = blockIdx.x * (uint32_t)(kKvThreads / LANES) + threadIdx.x / LANES;
-    const uint32_t heads = 2u * (uint32_t)a.kv_heads;
     const bool there = row < (uint32_t)a.rows;
-    const uint32_t token = there ? row / heads : 0;
-    const int head = there ? (int)(row - token * heads) : 0;
-    const bool is_k = head < a.kv_heads;
-    const int h = is_k ? head : head - a.kv_heads;
+    const uint32_t token = there ? row / (uint32_t)a.kv_heads : 0;
+    const int h = there ? (int)(row - token * (uint32_t)a.kv_heads) : 0;
     const int64_t slot = there ? a.slots[token] : -1;
-    const bool on = (uint64_t)slot < (uint64_t)(a.n_pages << a.log_page);
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    const int64_t page = slot >> a.log_page;
+    const int64_t at = ((page * a.kv_heads + h) << a.log_page) + (slot & ((1 << a.log_page) - 1));
+    const bool on = (uint64_t)slot < (uint64_t)(a.n_pages << a.log_page) &&
+                    QIFT_CK_RANGE(at, 1, (a.n_pages * a.kv_heads) << a.log_page);
+    uint32_t w[2][2] = {{0u, 0u}, {0u, 0u}};
+    float s[2] = {0.0f, 0.0f};
     if (on) {
-        const int64_t page = slot >> a.log_page;
-        const int64_t at = ((page * a.kv_heads + h) << a.log_page) + (slot & ((1 << a.log_page) - 1));
-        if (QIFT_CK_RANGE(at, 1, (a.n_pages * a.kv_heads) << a.log_page)) {
-            const uint8_t* codes = (is_k ? a.k_cache : a.v_cache) + at * (D / 2) + 4 * ts;
-            const uint32_t w[2] = {*reinterpret_cast<const uint32_t*>(codes), *reinterpret_cast<const uint32_t*>(codes + D / 4)};
-            const float s = (is_k ? a.k_scales : a.v_scales)[at];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int q = (int)(w[j >> 3] << (28 - 4 * (j & 7))) >> 28;  // sign-extended nibble
-                v[j] = __fmul_rn((float)q, s);
-            }
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t* codes = (kv ? a.v_cache : a.k_cache) + at * (D / 2) + 4 * ts;
+            w[kv][0] = *reinterpret_cast<const uint32_t*>(codes);
+            w[kv][1] = *reinterpret_cast<const uint32_t*>(codes + D / 4);
+            s[kv] = (kv ? a.v_scales : a.k_scales)[at];
         }
     }
-    row_hadamard16<D>(v, ts, a.block, a.norm);
-    if (!there) return;
-    uint4 packed[2];
-    __half2* h2 = reinterpret_cast<__half2*>(packed);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h2[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    __half* dst = (is_k ? a.k_out : a.v_out) + ((int64_t)token * a.kv_heads + h) * D + 8 * ts;
-    *reinterpret_cast<uint4*>(dst) = packed[0];
-    *reinterpret_cast<uint4*>(dst + D / 2) = packed[1];
+    for (int kv = 0; kv < 2; ++kv) {
+        // The nibble with its sign bit flipped, over 1.5 x 2^23: an fp32 whole number, and 1.5 x 2^23 + 8 off
+        // it the code, exactly; the conversion instruction has an eighth of the rate.
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t n = ((w[kv][j >> 3] >> (4 * (j & 7))) & 15u) ^ 0x4B400008u;
+            v[j] = __fmul_rn(__fsub_rn(__uint_as_float(n), 12582920.0f), s[kv]);
+        }
+        row_hadamard16<D>(v, ts, a.block, a.norm);
+        if (!there) continue;
+        uint4 packed[2];
+        __half2* h2 = reinterpret_cast<__half2*>(packed);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h2[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        __half* dst = (kv ? a.v_out : a.k_out) + (int64_t)row * D + 8 * ts;
+        *reinterpret_cast<uint4*>(dst) = packed[0];
+        *reinterpret_cast<uint4*>(dst + D / 2) = packed[1];
+    }
 }
 
 template <typename Kernel, typename Args>
@@ -279,8 +286,8 @@ static cudaError_t launch_append(AppendArgs a, cudaStream_t s) {
     }
     a.tokens_per_block = SLOTS / a.slots_per_token;
     const dim3 grid((unsigned)((a.tokens + a.tokens_per_block - 1) / a.tokens_per_block), parts);
-    return a.rope && a.rope_dim == D && !a.interleaved ? launch_rows(append_kv_kernel<D, true>, a, grid, s)
-                                                       : launch_rows(append_kv_kernel<D, false>, a, grid, s);
+    return a.rope && a.rope_dim == D && !a.interleaved && a.block == D ? launch_rows(append_kv_kernel<D, true>, a, grid, s)
+                                                                       : launch_rows(append_kv_kernel<D, false>, a, grid, s);
 }
 
 cudaError_t launch_append_kv(AppendArgs a, int head_dim, cudaStream_t s) {
