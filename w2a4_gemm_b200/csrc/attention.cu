@@ -16,7 +16,7 @@
 // (1032 + c, minus 1032); the other half stay at c + 72 and the row's 72 * sum(q) is taken off
 // beforehand as the accumulator's start value, which saves one operation in nine.  P^T needs
 // tokens along its other axis: movmatrix transposes it 8 x 8.  V^T is the left operand of the
-// second product, its codes paired over two tokens by byte permutes, and exact.
+// second product: transposing loads pair its codes over two tokens, and they are made exact.
 // Weights: t_j is multiplied into p_j before the rounding to binary16; the running reference is that
 // of u_j + log2 t_j, so the rounded weights lie in [0, 2^15] whatever the size of the values, and
 // keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
@@ -40,7 +40,7 @@ struct Shape {
     static constexpr int ROW = D / 2;                      // bytes of a key's codes
     static constexpr int STAGE = 2 * kStep * ROW + 2 * kStep * 4;
     static constexpr int STAGES = 2;
-    static constexpr int KW = D / 32, VW = D / 64;         // 32-bit words of a key, of a value, a lane holds
+    static constexpr int KW = D / 32;                      // 32-bit words of a key that a lane holds
     static constexpr int MT = D / 16;                      // 16-high tiles of O^T
     static constexpr int OPAD = D + 4;
     static constexpr int ring_bytes() { return kWarps * STAGES * STAGE; }
@@ -77,6 +77,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+__device__ __forceinline__ void ldmatrix4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
 }
 
 template <int BYTES>
@@ -208,19 +214,17 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     }
 
     // ---- the ring of this warp: lanes 0-15 copy the first 16 keys of a step, lanes 16-31 the rest.
-    // A lane's piece i (16 bytes) is piece c of key tok = l16 / CH + i * (16 / CH).  Keys lie in the order of
-    // the product's rows (row r is key (r & 8) + (r & 1) * 4 + (r & 7) / 2), and pieces are swapped so that the
-    // lanes' reads meet no bank twice; both are linear over the bits of the index, so a lane keeps the part
-    // of its own bits and the part of i is a constant.
+    // A lane's piece i (16 bytes) is piece c of key tok = l16 / CH + i * (16 / CH).  Pieces are swapped so that
+    // the lanes' reads meet no bank twice; the swap is linear over the bits of the key's number, so a lane keeps
+    // the part of its own bits and the part of i is a constant.
     uint8_t* ring = smem + warp * (S::STAGES * S::STAGE);
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int half = lane >> 4, l16 = lane & 15;
     constexpr int CH = S::ROW / 16;
-    auto row_of = [](int tok) { return (tok & 8) | ((tok & 3) << 1) | ((tok >> 2) & 1); };
-    auto k_swap = [](int r) { return D == 256 ? (r & 1) * 64 : 0; };
-    auto v_swap = [](int tok) { return D == 256 ? (tok & 3) * 32 : D == 128 ? ((tok >> 1) & 1) * 32 : 0; };
+    auto k_swap = [](int tok) { return D == 256 ? (tok & 1) * 64 : 0; };
+    auto v_swap = [](int tok) { return D == 256 ? (tok & 7) * 16 : D == 128 ? ((tok >> 1) & 3) * 16 : ((tok >> 2) & 1) * 16; };
     const int tok0 = l16 / CH, c0 = l16 % CH;
-    const uint32_t k_dst = ring32 + (half * 16 + row_of(tok0)) * S::ROW + ((c0 * 16) ^ k_swap(row_of(tok0)));
+    const uint32_t k_dst = ring32 + (half * 16 + tok0) * S::ROW + ((c0 * 16) ^ k_swap(tok0));
     const uint32_t v_dst = ring32 + (kStep + half * 16 + tok0) * S::ROW + ((c0 * 16) ^ v_swap(tok0));
     // A lane reads the scales of keys k8, k8 + 8, + 16, + 24 at once: they lie side by side.
     const uint32_t s_dst = ring32 + 2 * kStep * S::ROW + ((l16 & 7) * 4 + half * 2 + (l16 >> 3)) * 4;
@@ -257,8 +261,8 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
             const uint8_t* vs = v_src + (uint64_t)at * (16 * S::ROW);
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int tok = i * (16 / CH), r = row_of(tok);
-                cp16((k_dst + to + r * S::ROW) ^ k_swap(r), ks + i * 256);
+                const int tok = i * (16 / CH);
+                cp16((k_dst + to + tok * S::ROW) ^ k_swap(tok), ks + i * 256);
                 cp16((v_dst + to + tok * S::ROW) ^ v_swap(tok), vs + i * 256);
             }
             cp4(s_dst + to, ks_src + (uint64_t)at * 16);
@@ -278,8 +282,8 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
         cp_wait<S::STAGES - 1>();
         __syncwarp();
         const uint8_t* st = ring + stage * S::STAGE;
-        const float4 kf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW)[(g & 1) * 4 + (g >> 1)];
-        const float4 vf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW + kStep * 4)[(g & 1) * 4 + (g >> 1)];
+        const float4 kf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW)[g];
+        const float4 vf = reinterpret_cast<const float4*>(st + 2 * kStep * S::ROW + kStep * 4)[g];
         const bool all = (uint32_t)(s - sure_from) < sure_steps && !lost;
 
         // ---- scores
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = j0 + c * 16 + (g & 1) * 4 + (g >> 1) + 8 * e;
+                    const int j = j0 + c * 16 + g + 8 * e;
                     const bool in = there[c][e] >= 0.0f && j - base < range.limit;
                     bool any = false;
 #pragma unroll
@@ -396,35 +400,31 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
                     sum[n][1] += wt[c][n][2 * e + 1];
                     p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&wv[c][n][e]));
                 }
-            constexpr int VB = S::VW * 4;
-            uint32_t v[4][S::VW];
+            // Four codes of a key are a 16-bit unit; the transposing load of 8 keys by 8 units leaves unit g of
+            // keys 2t and 2t + 1 in a lane's register, as the left operand wants its pairs.  Four such loads an
+            // instruction: units 8 u + g of keys 0-7 and 8-15, for two u.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tok = t + 4 * i;  // product indexes 2t, 2t + 1, 2t + 8, 2t + 9
-                const int at = (D == 256 ? g * 16 : D == 128 ? g * 8 : g * 4) ^ v_swap(tok);
-                lds<VB>(v[i], st + kStep * S::ROW + (c * 16 + tok) * S::ROW + at);
-            }
+            for (int u = 0; u < S::MT / 2; u += 2) {
+                uint32_t v[4];
+                const int tok = (lane & 7) + ((lane >> 3) & 1) * 8, piece = (u + (lane >> 4)) * 16;
+                ldmatrix4t(v, ring32 + stage * S::STAGE + (kStep + c * 16 + tok) * S::ROW + (piece ^ v_swap(tok)));
 #pragma unroll
-            for (int w = 0; w < S::VW; ++w)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t lo = prmt(v[0][w], v[1][w], u ? 0x7632u : 0x5410u);
-                    uint32_t hi = prmt(v[2][w], v[3][w], u ? 0x7632u : 0x5410u);
+                for (int w = 0; w < 2; ++w)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const uint32_t lo = v[2 * w] >> (8 * e), hi = v[2 * w + 1] >> (8 * e);
                         const uint32_t a0 = nib.lo(lo), a1 = nib.hi(lo), a2 = nib.lo(hi), a3 = nib.hi(hi);
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) mma16816(o[n][w * 4 + u * 2 + e], a0, a1, a2, a3, p[n][0], p[n][1]);
-                        lo >>= 8, hi >>= 8;
+                        for (int n = 0; n < NR; ++n) mma16816(o[n][2 * (u + w) + e], a0, a1, a2, a3, p[n][0], p[n][1]);
                     }
-                }
+            }
         }
         stage = stage + 1 == S::STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
     __syncthreads();
 
-    // ---- join the warps.  Lane (g, t) holds values g * D/8 + 0 .. D/8 - 1 of rows 2t, 2t + 1.
+    // ---- join the warps.  Lane (g, t) holds values 32 u + 4 g + 0 .. 3 of rows 2t, 2t + 1.
     float* po = reinterpret_cast<float*>(smem);
     float* pm = po + kWarps * R * S::OPAD;
 #pragma unroll
@@ -434,11 +434,11 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
 #pragma unroll
             for (int m = 4; m < 32; m <<= 1) sum[n][q] += __shfl_xor_sync(0xffffffffu, sum[n][q], m);
             const int r = 8 * n + 2 * t + q;
-            float* dst = po + (warp * R + r) * S::OPAD + g * (D / 8);
+            float* dst = po + (warp * R + r) * S::OPAD + g * 4;
 #pragma unroll
-            for (int m = 0; m < S::MT; m += 2)
-                *reinterpret_cast<float4*>(dst + 2 * m) =
-                    make_float4(o[n][m][q], o[n][m][2 + q], o[n][m + 1][q], o[n][m + 1][2 + q]);
+            for (int u = 0; u < S::MT / 2; ++u)
+                *reinterpret_cast<float4*>(dst + 32 * u) =
+                    make_float4(o[n][2 * u][q], o[n][2 * u][2 + q], o[n][2 * u + 1][q], o[n][2 * u + 1][2 + q]);
             if (g == 0) {
                 pm[(warp * R + r) * 2] = refl[n][q];
                 pm[(warp * R + r) * 2 + 1] = sum[n][q];
