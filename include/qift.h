@@ -288,7 +288,8 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  * are rounded once to binary16 (2^-11 of each at most) for the tensor cores.  Scales in the cache lie in
  * [0, 65504/7], as qift_append_kv writes them.
  * qift_paged_attention_workspace returns the bytes for a call of these sizes, or -1 if qift_paged_attention
- * would refuse them.  head_dim, page_size: as above.  (max_pages * page_size + prefix_len) <= 2^30.
+ * would refuse them.  head_dim, page_size: as above.  max_pages * page_size + prefix_len <= 2^30;
+ * tokens * q_heads and batch * max_q * q_heads < 2^31.
  */
 int64_t qift_paged_attention_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                        int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages,

@@ -96,6 +96,15 @@ def test_attention_unsupported(L, kw):
     assert _attention(L, **kw) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("kw", [  # rows whose number passes 32 bits, or 64
+    dict(q_heads=65536, kv_heads=1, max_q=2 ** 31 - 1, batch=1, q_stride=65536 * 128),
+    dict(q_heads=65536, kv_heads=1, max_q=65536, batch=2 ** 31 - 1, q_stride=65536 * 128),
+    dict(q_heads=65536, kv_heads=1, max_q=2 ** 20, batch=2 ** 20, q_stride=65536 * 128),
+    dict(tokens=2 ** 27, prefix=A, prefix_len=64), dict(q_heads=65536, kv_heads=1, tokens=2 ** 16, prefix=A, prefix_len=64)])
+def test_attention_refuses_more_rows_than_it_can_number(L, kw):
+    assert _attention(L, **kw) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw", [dict(tokens=0), dict(batch=0, tokens=0), dict(max_q=0, tokens=0)])
 def test_attention_of_nothing_is_a_no_op(L, kw):
     assert _attention(L, **kw) == OK

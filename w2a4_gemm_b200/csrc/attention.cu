@@ -742,8 +742,9 @@ int debug_attention_path() { return g_attention_path; }
 
 bool attention_supported(const AttentionArgs& a) {
     if (debug_attention_path() == kAttentionWide && a.head_dim > 128) return false;
-    const attn::Deal d = attn::deal_out(a);
-    return d.blocks(a.batch, a.kv_heads) <= 0x7fffffff && (int64_t)a.batch * a.max_q * a.q_heads <= 0x7fffffff;
+    // Rows of the batch and of a launch in 32 bits, before anything is computed from their numbers.
+    if ((int64_t)a.batch * a.max_q > 0x7fffffff / a.q_heads || a.tokens > 0x7fffffff / a.q_heads) return false;
+    return attn::deal_out(a).blocks(a.batch, a.kv_heads) <= 0x7fffffff;
 }
 
 int64_t attention_workspace_bytes(const AttentionArgs& a) {
