@@ -280,7 +280,7 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *               domain, as qift_quantize_acts with block 0 takes it.
  *   out       : [tokens][q_heads][head_dim], out_dt QIFT_F16 (one rounding) or QIFT_F32.
  *   lse       : fp32 [tokens][q_heads] or NULL: log of the sum of exp(scale * q.k) over visible keys.
- *               A row that sees no key has out 0 and lse -infinity.
+ *               A row that sees no key has out 0 and lse -infinity; one whose q holds a NaN has NaN in both.
  *   workspace : device memory of at least qift_paged_attention_workspace() bytes (16-byte aligned),
  *               NULL where that is 0.  Two calls that may run at once, or captured graphs that may,
  *               need one each.

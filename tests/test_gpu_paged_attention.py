@@ -411,6 +411,24 @@ def test_peaked_scores():
     check(m)
 
 
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [5000, 300, 0]), ([9, 40], [2100, 1300])])
+def test_a_query_with_nan_or_infinity_is_not_hidden_and_spoils_no_other(q_lens, kv_lens, prefix):
+    m = make(q_lens, kv_lens, 8, 2, 64, 32, prefix, seed=12)
+    clean = dict(m, q=m["q"].clone())
+    m["q"][0, 1, 7], m["q"][1, 6, 63] = NAN, math.inf
+    ref, lse, A, reach = reference(clean)
+    good = torch.ones(m["q"].shape[:2], dtype=torch.bool, device="cuda")
+    good[0, 1] = good[1, 6] = False
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        l = torch.empty(m["q"].shape[:2], device="cuda")
+        out = call(m, out_dtype=torch.float32, lse=l)
+        assert ((out.double() - ref).abs() <= bound(A, reach, ref, False))[good].all(), path
+        assert torch.isnan(out[~good]).all() and torch.isnan(l[~good]).all(), path
+        assert not torch.isnan(l[good]).any()
+
+
 def test_rows_outside_every_sequence_are_left():
     m = make([1, 2, 1], [40, 50, 60], 4, 2, 64, 16, seed=11)
     m["q"] = torch.cat([m["q"], m["q"].flip(0)])           # four rows of padding behind

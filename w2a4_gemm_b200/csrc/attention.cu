@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
             const Parts p = parts(a, deal.slots);
             const int64_t at = (token * a.q_heads + head) * deal.slots + (prefix ? split : deal.prefix_splits + split);
             if (lane == 0) p.ml[at] = make_float2(M, L);
-            if (L > 0.0f) {
+            if (!(L == 0.0f)) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) p.o[at * D + lane * E + i] = acc[i];
             }
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
     float M = ml.x;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-    const float f = ml.y > 0.0f ? ex2(ml.x - M) : 0.0f;
+    const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
     float L = f * ml.y, acc[E];
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
             w[u] = __shfl_sync(0xffffffffu, f, (k0 + u) & 31);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
-            if (k0 + u < slots && w[u] > 0.0f) {  // an empty slot's O was never written
+            if (k0 + u < slots && !(w[u] == 0.0f)) {  // an empty slot's O was never written
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     *reinterpret_cast<float2*>(&v[u][e]) =
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     float L = 0.0f, acc[E];
     for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) {
         const float2 ml = p.ml[at + k];
-        const float f = ml.y > 0.0f ? ex2(ml.x - M) : 0.0f;
+        const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
         weight[k] = f;
         L += f * ml.y;
     }
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
             w[u] = k < slots ? weight[k] : 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
-            if (w[u] > 0.0f) {  // an empty slot's O was never written
+            if (!(w[u] == 0.0f)) {  // an empty slot's O was never written
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     *reinterpret_cast<float2*>(&v[u][e]) = *reinterpret_cast<const float2*>(p.o + (at + k) * D + lane * E + e);

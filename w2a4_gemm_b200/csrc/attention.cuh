@@ -11,7 +11,7 @@
 // Partial results of a row over a set S of keys, with u_j = scale log2(e) q.k_j:
 //   M, L = sum_S 2^(u_j - M), O = sum_S 2^(u_j - M) v_j
 // and any number of them join by M* = max M, L* = sum L 2^(M - M*), O* likewise.  An empty set has
-// M = kNone, L = 0.
+// M = kNone, L = 0, and no O; a row with a NaN or infinity in q has L = NaN, which stays one.
 #pragma once
 
 #include "common.cuh"
@@ -207,7 +207,7 @@ template <int D>
 __device__ __forceinline__ void finish_row(const AttentionArgs& a, float (&v)[D / 32], float M, float L, int64_t token,
                                            int head, int lane) {
     constexpr int E = D / 32;
-    const float inv = L > 0.0f ? __fdiv_rn(1.0f, L) : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= inv;
     row_hadamard<D>(v, lane, a.block, a.norm);
@@ -229,7 +229,7 @@ __device__ __forceinline__ void finish_row(const AttentionArgs& a, float (&v)[D 
                 *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
     if (a.lse && lane == 0)
-        a.lse[token * a.q_heads + head] = L > 0.0f ? 0.69314718056f * (M + log2f(L)) : -INFINITY;
+        a.lse[token * a.q_heads + head] = L == 0.0f ? -INFINITY : 0.69314718056f * (M + log2f(L));
 }
 
 }  // namespace attn

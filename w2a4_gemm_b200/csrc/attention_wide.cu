@@ -491,11 +491,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tc_fence_after();
             const bool finish = deal.slots == 0;
             const int block = finish ? a.block : 0;
-            const float by = (finish ? (sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f) : 1.0f) *
+            const float by = (finish ? (sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum)) : 1.0f) *
                              (block ? a.norm : 1.0f);
             int64_t at = token >= 0 ? token * a.q_heads + head : -1;
             if (finish) {
-                if (a.lse && token >= 0) a.lse[at] = sum > 0.0f ? 0.69314718056f * (ref + log2f(sum)) : -INFINITY;
+                if (a.lse && token >= 0) a.lse[at] = sum == 0.0f ? -INFINITY : 0.69314718056f * (ref + log2f(sum));
             } else if (token >= 0) {
                 at = at * deal.slots + (prefix ? split : deal.prefix_splits + split);
                 parts(a, deal.slots).ml[at] = make_float2(ref, sum);
