@@ -286,7 +286,8 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *               need one each.
  * Scores, the softmax's sums and the weighted sum are fp32; the weights, times their value's scale,
  * are rounded once to binary16 (2^-11 of each at most) for the tensor cores.  Scales in the cache lie in
- * [0, 65504/7], as qift_append_kv writes them.
+ * [0, 65504/7], as qift_append_kv writes them for finite rows; a key with another has an unspecified effect on
+ * the rows that see it and none on those that do not.
  * qift_paged_attention_workspace returns the bytes for a call of these sizes, or -1 if qift_paged_attention
  * would refuse them.  head_dim, page_size: as above.  max_pages * page_size + prefix_len <= 2^30;
  * tokens * q_heads and batch * max_q * q_heads < 2^31.

@@ -429,6 +429,25 @@ def test_a_query_with_nan_or_infinity_is_not_hidden_and_spoils_no_other(q_lens, 
         assert not torch.isnan(l[good]).any()
 
 
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_key_with_no_number_spoils_only_rows_that_see_it(d, window):
+    # rows of one block on both sides of it; scales of keys, of values and of both
+    m = make([40], [200], 4, 1, d, 16, seed=d)
+    ref, _, A, reach = reference(m, window)
+    positions = torch.arange(160, 200, device="cuda")
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        for bad, ks, vs in ((178, math.inf, 1.0), (178, 1.0, math.inf), (193, NAN, NAN), (166, math.inf, NAN)):
+            cache = [c.clone() for c in m["cache"]]
+            cache[1][m["table"][0, bad // 16], 0, bad % 16] = ks
+            cache[3][m["table"][0, bad // 16], 0, bad % 16] = vs
+            out = call(dict(m, cache=cache), window=window, out_dtype=torch.float32)
+            see = (positions >= bad) & ((positions < bad + window) if window else True)
+            err = (out.double() - ref).abs()
+            assert (err <= bound(A, reach, ref, False))[~see].all(), (path, bad, ks, vs)
+
+
 def test_rows_outside_every_sequence_are_left():
     m = make([1, 2, 1], [40, 50, 60], 4, 2, 64, 16, seed=11)
     m["q"] = torch.cat([m["q"], m["q"].flip(0)])           # four rows of padding behind

@@ -319,7 +319,8 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
             }
         }
         // Masked scores become -infinity (their scale, which may hold anything, is multiplied in first), and
-        // what no row sees gets the value scale 0.
+        // what no row sees gets the value scale 0.  A value scale that is no number would reach the rows that do
+        // not see it by 0 times it: it goes into the score instead, of the rows that do.
         if (!all) {
             const int j0 = base + (s + (s >= range.head ? shift : 0)) * kStep;  // position of the step's first key
             const float there[2][2] = {{kf.x, kf.y}, {kf.z, kf.w}};
@@ -329,6 +330,8 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + c * 16 + g + 8 * e;
                     const bool in = there[c][e] >= 0.0f && j - base < range.limit;
+                    const bool odd = !(vs[c][e] <= 65504.0f);
+                    const float k1 = odd ? __int_as_float(0x7fffffff) : ks[c][e];
                     bool any = false;
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
@@ -336,11 +339,11 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
                         for (int q = 0; q < 2; ++q) {
                             const int p = pos[n][q];
                             const bool see = in && j <= p && (!a.window || j > p - a.window || j < a.sinks);
-                            x[c][n][2 * e + q] = see ? x[c][n][2 * e + q] * ks[c][e] : -INFINITY;
+                            x[c][n][2 * e + q] = see ? x[c][n][2 * e + q] * k1 : -INFINITY;
                             any |= see;
                         }
                     ks[c][e] = 1.0f;
-                    if (!any) vs[c][e] = 0.0f;
+                    if (!any || odd) vs[c][e] = 0.0f;
                 }
         }
 

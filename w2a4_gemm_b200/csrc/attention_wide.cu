@@ -196,8 +196,8 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&x)[32]) {
                  : "memory");
 }
 
-// A scale of the cache.  What none can be (a row that was never written) counts as 0.
-__device__ __forceinline__ float scale_of(float s) { return s >= 0.0f && s <= 9358.0f ? s : 0.0f; }
+// Whether s can be a scale of the cache.
+__device__ __forceinline__ bool is_scale(float s) { return s >= 0.0f && s <= 9358.0f; }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&x)[16]) {
     asm volatile(
@@ -596,8 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ks = is ? reinterpret_cast<const float*>(smem + S::KS_AT)[u] : 0.0f;
             const float vs = is ? reinterpret_cast<const float*>(smem + S::VS_AT)[u] : 0.0f;
             // S of step i - 2 is done, so both tiles' softmax is past step i - 3: this place of the ring is free.
-            const float t = scale_of(vs);
-            key_scales[ring * BN + u] = scale_of(ks) * a.scale_log2;
+            // What is no scale becomes NaN in the scores of the rows that see the key; as a value scale it would
+            // reach the others, by 0 times it.
+            const bool good = is_scale(ks) && is_scale(vs);
+            const float t = good ? vs : 0.0f;
+            key_scales[ring * BN + u] = good ? ks * a.scale_log2 : __int_as_float(0x7fffffff);
             value_scales[ring * BN + u] = t;
             float top = t;  // of this warp's 32 keys
 #pragma unroll
