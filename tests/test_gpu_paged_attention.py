@@ -456,6 +456,22 @@ def test_rows_outside_every_sequence_are_left():
     check(m)
 
 
+@pytest.mark.parametrize("q_lens", [[1] * 20, [3, 0, 70, 5]])
+def test_padding_before_and_behind_with_a_prefix(q_lens):
+    m = make(q_lens, [400 + n for n in q_lens], 4, 1, 64, 32, prefix=390, seed=13)
+    T, ahead, behind = sum(q_lens), 7, 90
+    pad = lambda n: torch.full((n, 4, 64), NAN, device="cuda").half()
+    ref, _, A, reach = reference(m)
+    padded = dict(m, q=torch.cat([pad(ahead), m["q"], pad(behind)]), cu_q=m["cu_q"] + ahead)
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        out, l = torch.full((T + ahead + behind, 4, 64), 77.0, device="cuda"), torch.full((T + ahead + behind, 4), 77.0, device="cuda")
+        call(padded, out=out, lse=l, out_dtype=torch.float32)
+        assert ((out[ahead:ahead + T].double() - ref).abs() <= bound(A, reach, ref, False)).all(), path
+        for x in (out, l):
+            assert (x[:ahead] == 77).all() and (x[ahead + T:] == 77).all()
+
+
 def test_pages_that_are_not_there():
     m = make([1, 1, 1], [100, 80, 40], 4, 2, 128, 16, seed=12)
     m["table"][0, 2], m["table"][1, 0], m["table"][2, 0] = -1, 2 ** 31 - 1, m["cache"][0].shape[0]

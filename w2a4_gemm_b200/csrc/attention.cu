@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
         int pos = -1;
         if (prefix) {
             if (r < a.tokens * G) token = r / G, pos = position_of(a, token);
+            if (pos < -1) token = pos = -1;
         } else {
             const Sequence s = sequence(a, b);
             if (r < (int64_t)s.q_len * G) {

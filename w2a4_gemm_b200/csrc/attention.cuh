@@ -79,10 +79,11 @@ __device__ __forceinline__ int sequence_of(const AttentionArgs& a, int64_t token
     return b >= 0 && token < a.cu_q[b + 1] ? b : -1;
 }
 
-// Position of a token in its sequence, or -1 (it sees nothing).
+// Position of a token in its sequence, -1 (it sees nothing) or, if it belongs to no sequence, -2: such rows are
+// left out, since one that sees nothing would have every step of its block masked.
 __device__ __forceinline__ int position_of(const AttentionArgs& a, int64_t token) {
     const int b = sequence_of(a, token);
-    if (b < 0) return -1;
+    if (b < 0) return -2;
     const Sequence s = sequence(a, b);
     const int64_t p = (int64_t)s.kv_len - s.q_len + (token - s.first);
     return p < 0 ? -1 : (int)p;

@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t row = ((int64_t)pair * TILES + tile) * BM + r;
         if (prefix) {
             if (row < a.tokens * G) token = row / G, pos = position_of(a, token);
+            if (pos < -1) token = pos = -1;
         } else {
             const Sequence s = sequence(a, b);
             if (row < (int64_t)s.q_len * G) {
