@@ -278,7 +278,8 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *   scale     : softmax scale, usually 1 / sqrt(head_dim).
  *   block     : the result is rotated back by Hadamard blocks of `block`; 0 leaves it in the cache's
  *               domain, as qift_quantize_acts with block 0 takes it.
- *   out       : [tokens][q_heads][head_dim], out_dt QIFT_F16 (one rounding) or QIFT_F32.
+ *   out       : [tokens][q_heads][head_dim], out_dt QIFT_F16 (one rounding) or QIFT_F32; must not
+ *               overlap q.
  *   lse       : fp32 [tokens][q_heads] or NULL: log of the sum of exp(scale * q.k) over visible keys.
  *               A row that sees no key has out 0 and lse -infinity; one whose q holds a NaN has NaN in both.
  *   workspace : device memory of at least qift_paged_attention_workspace() bytes (16-byte aligned),

@@ -96,6 +96,12 @@ def test_attention_unsupported(L, kw):
     assert _attention(L, **kw) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("out,dt", [(0, 1), (6 * 8192 - 16, 1), (-6 * 8192 + 16, 1), (-6 * 16384 + 16, 0)])
+def test_attention_refuses_a_result_over_its_queries(L, out, dt):
+    assert _attention(L, out=A + out, dt=dt, tokens=6) == BAD
+    assert _attention(L, q=A << 8, out=A, ws=None, prefix=A, prefix_len=5) == BAD  # apart: only the workspace is missing
+
+
 @pytest.mark.parametrize("kw", [  # rows whose number passes 32 bits, or 64
     dict(q_heads=65536, kv_heads=1, max_q=2 ** 31 - 1, batch=1, q_stride=65536 * 128),
     dict(q_heads=65536, kv_heads=1, max_q=65536, batch=2 ** 31 - 1, q_stride=65536 * 128),

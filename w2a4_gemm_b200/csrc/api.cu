@@ -434,6 +434,9 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
         return QIFT_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride < (int64_t)q_heads * head_dim || q_stride > INT64_MAX / 4 / tokens)
         return QIFT_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)q_heads * head_dim;  // a block reads its queries while another may have written its rows
+    if (overlap(out, tokens * row * (out_dt == QIFT_F16 ? 2 : 4), q, ((tokens - 1) * q_stride + row) * 2))
+        return QIFT_ERR_INVALID_ARG;
     const int64_t need = qift::attention_workspace_bytes(a);
     if (need > 0 && (!workspace || workspace_bytes < need)) return QIFT_ERR_INVALID_ARG;
     a.q = static_cast<const __half*>(q);
