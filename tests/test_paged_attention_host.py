@@ -1,6 +1,7 @@
 """Host-side checks of the paged KV4 cache's entry points: what they refuse, before anything is launched, and
 what the workspace query answers (no call here reaches a kernel)."""
 import ctypes as C
+import threading
 
 import pytest
 import torch
@@ -140,6 +141,43 @@ def test_binding_refuses_cpu_tensors():
         q.qift_gather_kv(*c, s, 64)
     with pytest.raises(ValueError):
         q.qift_paged_attention(x, None, 1, *c, torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv", "prefix_len", "window", "sinks", "page_size", "q_heads"])
+def test_sizes_past_32_bits_are_refused_not_cut(name):
+    a = dict(tokens=1, q_heads=32, kv_heads=8, head_dim=128, batch=1, max_q=1, page_size=16, max_pages=4, max_kv=0,
+             prefix_len=0, window=0, sinks=0)
+    assert q.qift_paged_attention_workspace(**a) >= 0
+    for more in (2 ** 32, 2 ** 31):
+        with pytest.raises(ValueError, match=name):
+            q.qift_paged_attention_workspace(**{**a, name: a[name] + more})
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 32 + 3), dict(sinks=2 ** 32), dict(block=2 ** 32), dict(max_kv=2 ** 33 + 1),
+                                dict(prefix_len=2 ** 32), dict(max_q=2 ** 32 + 1), dict(window=-2 ** 32)])
+def test_binding_refuses_sizes_past_32_bits(kw):
+    c = [torch.zeros(2, 1, 16, 32, dtype=torch.uint8), torch.zeros(2, 1, 16)] * 2
+    x = torch.zeros(1, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="32 bits"):
+        q.qift_paged_attention(x, None, **{"max_q": 1, **kw}, k_cache=c[0], k_scales=c[1], v_cache=c[2], v_scales=c[3],
+                               page_table=torch.zeros(1, 1, dtype=torch.int32), kv_lens=torch.ones(1, dtype=torch.int32))
+    if "block" in kw:
+        with pytest.raises(ValueError, match="32 bits"):
+            q.qift_append_kv(x, x, torch.zeros(1, dtype=torch.int64), kw["block"], *c)
+        with pytest.raises(ValueError, match="32 bits"):
+            q.qift_gather_kv(*c, torch.zeros(1, dtype=torch.int64), kw["block"])
+
+
+def test_a_pin_of_one_thread_leaves_another_threads_answers(L):
+    size, sizes = q.qift_paged_attention_workspace, (1, 32, 8, 128, 1, 1, 16, 512)
+    want, got = size(*sizes), []
+    def pinned():
+        q.qift_debug_set_attention_path("wide")
+        got.append(size(*sizes))
+    t = threading.Thread(target=pinned)
+    t.start()
+    t.join()
+    assert got[0] != want and size(*sizes) == want
 
 
 def test_attention_path_pin(L):

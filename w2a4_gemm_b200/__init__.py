@@ -16,6 +16,7 @@ import ctypes as C
 import functools
 import math
 import os
+import threading
 
 import torch
 
@@ -400,6 +401,13 @@ def _cache(k_cache, k_scales, v_cache, v_scales):
     return at, (shape[0], shape[1], shape[2], 2 * shape[3]), index
 
 
+def _int32(**values):
+    """Refuses what the library's 32-bit arguments would cut to another value."""
+    for name, x in values.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
+
+
 def _launch(index: int, stream, fn, *args) -> int:
     """Calls the library's `fn` on `stream` (None: the current one of device `index`) with that device current."""
     if stream is None:
@@ -426,6 +434,7 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
     fp32 ``[pages, kv_heads, page_size]`` are written at ``slots`` (int64, ``page * page_size + offset``; -1 =
     padding).  ``rope`` fp32 ``[positions, rope_dim]`` holds cosines, then sines, and ``positions`` (int64) its row
     for each token.  Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
+    _int32(block=block)
     (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
     k_at, k_row = _heads(k, "k", (T, kv_heads, d), index)
@@ -462,6 +471,7 @@ def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch
                    slots: torch.Tensor, block: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows of a paged KV4 cache read back, rotated back by ``block`` (0: in the cache's domain): fp16
     ``(k, v)``, each ``[tokens, kv_heads, head_dim]``; zeros for slots outside the cache."""
+    _int32(block=block)
     (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() else 0
     slots_at = _is(slots, "slots", torch.int64, (T,), index)
@@ -490,6 +500,8 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     0 takes it).  ``lse`` (fp32 ``[tokens, q_heads]``), if given, receives the log-sum-exp.  ``workspace`` (uint8,
     ``qift_paged_attention_workspace`` bytes) is allocated on the call's stream if not given.  Rows of a new result
     that belong to no sequence are not initialised."""
+    if not 0 <= (max_q | window | sinks | prefix_len | max_kv | block) < 2 ** 31:
+        _int32(max_q=max_q, window=window, sinks=sinks, prefix_len=prefix_len, max_kv=max_kv, block=block)
     (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [tokens, q_heads, head_dim] tensor")
@@ -540,8 +552,15 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     return out
 
 
-@functools.lru_cache(maxsize=1024)
+_kernel_pin = threading.local()  # the answer is the pinned kernel's, and a pin is a thread's
+
+
 def _workspace_bytes(*sizes: int) -> int:
+    return _workspace_bytes_of(getattr(_kernel_pin, "path", 0), *sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes_of(path: int, *sizes: int) -> int:
     return lib().qift_paged_attention_workspace(*sizes)
 
 
@@ -549,6 +568,8 @@ def qift_paged_attention_workspace(tokens: int, q_heads: int, kv_heads: int, hea
                                    page_size: int, max_pages: int, max_kv: int = 0, prefix_len: int = 0,
                                    window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace that ``qift_paged_attention`` needs for these sizes; raises if it would refuse them."""
+    _int32(q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, batch=batch, max_q=max_q, page_size=page_size,
+           max_pages=max_pages, max_kv=max_kv, prefix_len=prefix_len, window=window, sinks=sinks)
     n = _workspace_bytes(tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv, prefix_len,
                          window, sinks)
     if n < 0:
@@ -614,7 +635,7 @@ def qift_debug_set_attention_path(path) -> None:
     """Test hook: pin qift_paged_attention's kernel in this thread ("auto", "stream", "wide")."""
     p = ATTENTION_PATHS[path] if isinstance(path, str) else int(path)
     _check(lib().qift_debug_set_attention_path(p), "qift_debug_set_attention_path")
-    _workspace_bytes.cache_clear()  # the answer is the pinned kernel's
+    _kernel_pin.path = p
 
 
 def qift_debug_set_pdl(enable: bool) -> None:
