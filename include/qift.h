@@ -229,8 +229,7 @@ qift_status qift_decode_linear(const void* x, int64_t tokens, int64_t n_in, int3
  *   positions : int64 [tokens], rows of `rope` (NULL if rope is NULL).
  *   slots     : int64 [tokens], all different.  A token whose slot is outside the cache (-1 marks
  *               padding) is not written; one whose position is outside [0, rope_len) is neither
- *               written nor is its q_out row.  If a slot is named twice, which row it holds is
- *               unspecified.
+ *               written nor is its q_out row.  What a slot holds that is named twice is unspecified.
  *   block     : Hadamard block as in qift_rotate, at most head_dim; 0 = none.
  *   q_out     : fp16 [tokens][q_heads][head_dim] out, the rotated queries that
  *               qift_paged_attention takes; must not overlap q, k or v.
