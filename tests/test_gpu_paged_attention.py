@@ -349,6 +349,29 @@ def test_sequences_that_end_inside_the_prefix():
     check(m, 20, 3)
 
 
+@pytest.mark.parametrize("hq,hk,d,prefix,window", [(8, 2, 128, 0, 0), (8, 2, 64, 0, 50), (4, 1, 128, 300, 0), (16, 1, 64, 0, 0),
+                                                    (24, 1, 64, 0, 0), (2, 1, 256, 70, 0), (2, 2, 64, 300, 90)])
+@pytest.mark.parametrize("far", [400, 3000])
+def test_long_sequences_among_short_ones(hq, hk, d, prefix, window, far):
+    # each sequence's row tiles are found through the offsets, and its length chooses its kernel
+    q_lens = [0, 1] + [1] * 20 + [500] + [1, 2, 0, 3] * 4 + [90, 0, 1] + [1] * 30
+    kv_lens = [n + prefix + (37 * i * i) % far for i, n in enumerate(q_lens)]
+    kv_lens[5], kv_lens[7] = 0, 1
+    m = make(q_lens, kv_lens, hq, hk, d, 32, prefix, seed=hq + d)
+    check(m, window, 3 if window else 0, dtypes=(torch.float16,))
+    ref, lse, A, reach = reference(m, window, 3 if window else 0)
+    T, behind = sum(q_lens), 150
+    q = torch.cat([torch.full((3, hq, d), NAN, device="cuda").half(), m["q"], torch.full((behind, hq, d), NAN, device="cuda").half()])
+    out = torch.full(q.shape, 77.0, device="cuda")
+    l = torch.full(q.shape[:2], 77.0, device="cuda")
+    call(dict(m, q=q, cu_q=m["cu_q"] + 3), window=window, sinks=3 if window else 0, out=out, out_dtype=torch.float32, lse=l)
+    assert ((out[3:3 + T].double() - ref).abs() <= bound(A, reach, ref, False)).all()
+    none = lse.isinf()
+    assert torch.equal(l[3:3 + T] == -math.inf, none) and (out[3:3 + T][none] == 0).all()
+    for x in (out, l):
+        assert (x[:3] == 77).all() and (x[3 + T:] == 77).all()
+
+
 def test_an_empty_sequence_among_long_ones_sees_nothing():
     # the prefix's rows are those of the whole batch: one that sees nothing lies between rows that see all
     m = make([1] * 9 + [3], [400 + b for b in range(4)] + [0] + [500 + b for b in range(4)] + [2], 4, 2, 128, 16,

@@ -118,13 +118,20 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     const bool prefix = id < prefix_blocks;
     if (!prefix) id -= prefix_blocks;
     const int splits = prefix ? deal.prefix_splits : deal.own_splits;
-    const int tiles = prefix ? deal.prefix_tiles : deal.own_tiles;
     const int split = (int)(id % splits);
     id /= splits;
     const int h = (int)(id % a.kv_heads);
     id /= a.kv_heads;
-    const int tile = (int)(id % tiles);
-    const int b = (int)(id / tiles);  // own only
+    int tile, b = 0;  // b: own only
+    if (prefix) {
+        tile = (int)id;
+    } else if (deal.own_ragged) {
+        if (!ragged_tile<R>(a, id, G, b, tile)) return;
+    } else {
+        tile = (int)(id % deal.own_tiles);
+        b = (int)(id / deal.own_tiles);
+        if (deal.few && !deal.is_few((int64_t)sequence(a, b).q_len * G)) return;
+    }
     const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
     const int base = prefix ? 0 : a.prefix_len;
     const int64_t capacity = prefix ? a.prefix_len : (int64_t)a.max_pages << a.log_page;
@@ -482,25 +489,34 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     }
 }
 
+// The row-th row to be joined: its token (-1: none), head and number of partial results.  Rows are dealt out as
+// (sequence, token, head), or as (token, head) where that is much less.
+__device__ __forceinline__ int64_t joined_row(const AttentionArgs& a, const Deal& deal, bool by_token, int64_t row, int& head,
+                                              int& slots) {
+    head = (int)(row % a.q_heads);
+    row /= a.q_heads;
+    const int64_t b = by_token ? (row < a.tokens ? sequence_of(a, row) : -1) : row / a.max_q;
+    if (b < 0 || b >= a.batch) return -1;
+    const Sequence s = sequence(a, (int)b);
+    const int64_t i = by_token ? row - s.first : row % a.max_q;
+    if (i < 0 || i >= s.q_len) return -1;
+    slots = deal.prefix_splits + (deal.is_few((int64_t)s.q_len * (a.q_heads / a.kv_heads)) ? deal.few_splits : deal.own_splits);
+    return s.first + i;
+}
+
 // The same for rows of up to 32 slots, a warp a row: a lane holds a slot's weight.  (4096 rows of 10 slots, a
 // block each: 17.8 us.)
 template <int D>
-__global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, const int slots) {
+__global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, const Deal deal, const bool by_token) {
     constexpr int E = D / 32;
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-    int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int head = (int)(row % a.q_heads);
-    row /= a.q_heads;
-    const int i = (int)(row % a.max_q);
-    const int64_t b = row / a.max_q;
-    if (b >= a.batch) return;
-    const Sequence s = sequence(a, (int)b);
-    if (i >= s.q_len) return;
-    const int64_t token = s.first + i;
-    const Parts p = parts(a, slots);
-    const int64_t at = (token * a.q_heads + head) * slots;
+    int head, slots;
+    const int64_t token = joined_row(a, deal, by_token, (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), head, slots);
+    if (token < 0) return;
+    const Parts p = parts(a, deal.slots);
+    const int64_t at = (token * a.q_heads + head) * deal.slots;
     const float2 ml = lane < slots ? p.ml[at + lane] : make_float2(kNone, 0.0f);
     float M = ml.x;
 #pragma unroll
@@ -533,30 +549,25 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
     finish_row<D>(a, acc, M, L, token, head, lane);
 }
 
-// Joins the partial results of a row, one block a row; rows are dealt out as (sequence, token, head).
+// Joins the partial results of a row, one block a row.
 // All (M, L) are read at once and become weights in shared memory, then each warp sums every
 // kJoinWarps-th slot with four loads in flight: what it costs is the chain of loads, so the chain is
 // kept short (32 rows of 74 slots took 14.5 us with one load in flight and four warps).
 constexpr int kJoinWarps = 8;
 constexpr int kMostSlots = 4096;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionArgs a, const int slots) {
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionArgs a, const Deal deal, const bool by_token) {
     constexpr int E = D / 32;
     extern __shared__ float weight[];
     __shared__ float part[kJoinWarps][D], red[2][kJoinWarps];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t row = blockIdx.x;
-    const int head = (int)(row % a.q_heads);
-    row /= a.q_heads;
-    const int i = (int)(row % a.max_q);
-    const int64_t b = row / a.max_q;
-    const Sequence s = sequence(a, (int)b);
-    if (i >= s.q_len) return;
-    const int64_t token = s.first + i;
-    const Parts p = parts(a, slots);
-    const int64_t at = (token * a.q_heads + head) * slots;
+    int head, slots;
+    const int64_t token = joined_row(a, deal, by_token, blockIdx.x, head, slots);
+    if (token < 0) return;
+    const Parts p = parts(a, deal.slots);
+    const int64_t at = (token * a.q_heads + head) * deal.slots;
     float M = kNone;
     for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) M = fmaxf(M, p.ml[at + k].x);
 #pragma unroll
@@ -616,23 +627,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
 // How one kind of row sets (the prefix's, or the sequences' own) is cut into blocks.
 struct Cut {
     int tiles, splits, chunk;
-    double us;  // what it takes, roughly
+    int64_t sets;  // row tiles of all row sets
+    bool ragged;
+    double us;     // what it takes, roughly
 };
-// `sets` row sets of `rows` rows and at most `keys` keys, on the streaming kernel (`per` rows a block) or the
-// one for many rows.
+// `batch` row sets of up to `rows` rows, `all_rows` in all, and at most `keys` keys, for each kv head, on the
+// streaming kernel (`per` rows a block) or the one for many rows.
 // Streaming: a split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths, at most 4096.
 // Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by 8 kv heads
 // took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the bound on their
 // lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with one turn, 179
 // with two and 174 with four.
 // Many rows: one block an SM, split only where there are fewer row sets than SMs.
-static Cut cut(bool wide, int per, int64_t sets, int64_t rows, int64_t keys, bool equal, int head_dim) {
+static Cut cut(bool wide, int per, int64_t kv_heads, int64_t batch, int64_t rows, int64_t all_rows, int64_t keys, bool equal,
+               int head_dim) {
     Cut c = {};
     const int64_t step = wide ? kWideStep : kStep;
     const int64_t least = 512 / step, most = wide || equal ? 1 << 20 : 4096 / step;
     const int64_t steps = (keys + step - 1) / step + 1;
     c.tiles = (int)((rows + per - 1) / per);
-    const int64_t blocks = sets * c.tiles;
+    c.sets = batch * c.tiles;
+    const int64_t total = all_rows / per + batch;  // never less than the tiles of equal sets
+    c.ragged = 2 * total <= c.sets;                // a search through the offsets, for half of the blocks
+    if (c.ragged) c.sets = total;
+    const int64_t blocks = kv_heads * c.sets;
     int64_t n = wide ? 148 / blocks : (equal ? 1 : 2) * 592 / blocks;
     n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
     n = std::min<int64_t>(n, kMostSlots / 2);
@@ -650,7 +668,7 @@ static Cut cut(bool wide, int per, int64_t sets, int64_t rows, int64_t keys, boo
 // Rows of a block of the streaming kernel.
 static int stream_rows(const AttentionArgs& a, const Deal& d) {
     const int64_t G = a.q_heads / a.kv_heads;
-    return (d.own_wide || a.max_q * G <= 8) && (d.prefix_wide || !a.prefix_len || a.tokens * G <= 8) ? 8 : 16;
+    return (d.few ? d.few <= 8 : d.own_wide || a.max_q * G <= 8) && (d.prefix_wide || !a.prefix_len || a.tokens * G <= 8) ? 8 : 16;
 }
 
 // Which kernel takes what: the one that takes less by the measure above.  A step of 256 rows costs the same
@@ -663,28 +681,46 @@ static Deal deal_out(const AttentionArgs& a) {
     if (a.window)  // rows of the whole batch stand far apart: no such bound on what they see of the prefix
         own = std::min(own, (int64_t)a.window + a.max_q + a.sinks + 2 * kStep);
     own = std::max<int64_t>(own, 1);
-    const int64_t own_sets = (int64_t)a.batch * a.kv_heads;
-    auto own_cut = [&](bool wide, int per) { return cut(wide, wide ? kWideRows : per, own_sets, own_rows, own, equal, a.head_dim); };
-    auto shared_cut = [&](bool wide, int per) {
-        return cut(wide, wide ? kWideRows : per, a.kv_heads, shared_rows, a.prefix_len, true, a.head_dim);
+    auto own_cut = [&](bool wide, int per) {
+        return cut(wide, wide ? kWideRows : per, a.kv_heads, a.batch, own_rows, shared_rows, own, equal, a.head_dim);
     };
+    auto shared_cut = [&](bool wide, int per) {
+        return cut(wide, wide ? kWideRows : per, a.kv_heads, 1, shared_rows, shared_rows, a.prefix_len, true, a.head_dim);
+    };
+    Cut own_is = {};
     Deal d = {};
     const int pin = debug_attention_path();
     if (pin == kAttentionWide) {
         d.own_wide = true;
         d.prefix_wide = a.prefix_len > 0;
     } else if (a.head_dim <= 128 && pin == kAttentionAuto) {
-        d.own_wide = own_rows > 16 && own_cut(true, 0).us < own_cut(false, 16).us;
+        const Cut many = own_cut(true, 0), few = own_cut(false, 16);
+        d.own_wide = own_rows > 16 && many.us < few.us;
+        if (own_rows > 16 && G <= 16 && many.ragged) {
+            // Long sequences among short ones (prompts among single tokens): each to its kernel, if one long
+            // sequence with all the rows and single tokens of the others would be faster so.  Blocks of the
+            // kernel for many rows that find a short sequence leave at once (about 1 us of an SM).
+            const int most = G <= 8 ? 8 : 16;
+            const Cut one = cut(true, kWideRows, a.kv_heads, 1, shared_rows, shared_rows, own, equal, a.head_dim);
+            const Cut rest = cut(false, most, a.kv_heads, a.batch, most, most * (int64_t)a.batch, own, equal, a.head_dim);
+            if (one.us + rest.us + (double)a.batch * a.kv_heads * one.splits / 148 < std::min(many.us, few.us)) {
+                d.own_wide = true;
+                d.few = most, d.few_splits = rest.splits, d.few_chunk = rest.chunk;
+                own_is = one;
+                own_is.sets = many.sets, own_is.ragged = true;
+            }
+        }
         d.prefix_wide = a.prefix_len && shared_rows > 16 && shared_cut(true, 0).us < shared_cut(false, 16).us;
     }
     const int per = stream_rows(a, d);
-    const Cut c = own_cut(d.own_wide, per);
-    d.own_tiles = c.tiles, d.own_splits = c.splits, d.own_chunk = c.chunk;
+    const Cut c = d.few ? own_is : own_cut(d.own_wide, per);
+    d.own_tiles = c.tiles, d.own_splits = c.splits, d.own_chunk = c.chunk, d.own_sets = c.sets, d.own_ragged = c.ragged;
     if (a.prefix_len) {
         const Cut p = shared_cut(d.prefix_wide, per);
         d.prefix_tiles = p.tiles, d.prefix_splits = p.splits, d.prefix_chunk = p.chunk;
     }
-    d.slots = a.prefix_len || d.own_splits > 1 ? d.prefix_splits + d.own_splits : 0;
+    const int splits = std::max(d.own_splits, d.few_splits);
+    d.slots = a.prefix_len || splits > 1 ? d.prefix_splits + splits : 0;
     return d;
 }
 
@@ -694,7 +730,7 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
     const cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)d.blocks(a.batch, a.kv_heads));
+    cfg.gridDim = dim3((unsigned)d.blocks(a.kv_heads));
     cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -707,9 +743,11 @@ static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStre
 }
 
 template <int D>
-static cudaError_t launch_join(const AttentionArgs& a, int slots, cudaStream_t s) {
+static cudaError_t launch_join(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    const int64_t rows = (int64_t)a.batch * a.max_q * a.q_heads;
+    const int slots = d.slots;
+    const bool by_token = 2 * a.tokens <= (int64_t)a.batch * a.max_q;
+    const int64_t rows = (by_token ? a.tokens : (int64_t)a.batch * a.max_q) * a.q_heads;
     const bool few = slots <= 32 && rows >= 148 * 2;  // a warp a row only where that fills the GPU
     cfg.gridDim = dim3((unsigned)(few ? (rows + 7) / 8 : rows));
     cfg.blockDim = dim3(few ? 256 : 32 * kJoinWarps);
@@ -720,22 +758,20 @@ static cudaError_t launch_join(const AttentionArgs& a, int slots, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, few ? join_few_kernel<D> : join_kernel<D>, a, slots);
+    return cudaLaunchKernelEx(&cfg, few ? join_few_kernel<D> : join_kernel<D>, a, d, by_token);
 }
 
 template <int D>
 static cudaError_t launch_all(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
     for (const bool wide : {true, false}) {  // one launch for each kernel that has rows to do
-        Deal part = d;
-        if (d.prefix_wide != wide) part.prefix_tiles = 0;
-        if (d.own_wide != wide) part.own_tiles = 0;
-        if (part.blocks(a.batch, a.kv_heads) == 0) continue;
+        const Deal part = d.of(wide, a.batch);
+        if (part.blocks(a.kv_heads) == 0) continue;
         const cudaError_t e = wide                     ? launch_wide(a, part, s)
                               : stream_rows(a, d) == 8 ? launch_stream<D, 1>(a, part, s)
                                                     : launch_stream<D, 2>(a, part, s);
         if (e != cudaSuccess) return e;
     }
-    return d.slots ? launch_join<D>(a, d.slots, s) : cudaSuccess;
+    return d.slots ? launch_join<D>(a, d, s) : cudaSuccess;
 }
 
 }  // namespace attn
@@ -748,7 +784,8 @@ bool attention_supported(const AttentionArgs& a) {
     if (debug_attention_path() == kAttentionWide && a.head_dim > 128) return false;
     // Rows of the batch and of a launch in 32 bits, before anything is computed from their numbers.
     if ((int64_t)a.batch * a.max_q > 0x7fffffff / a.q_heads || a.tokens > 0x7fffffff / a.q_heads) return false;
-    return attn::deal_out(a).blocks(a.batch, a.kv_heads) <= 0x7fffffff;
+    const attn::Deal d = attn::deal_out(a);
+    return d.of(true, a.batch).blocks(a.kv_heads) <= 0x7fffffff && d.of(false, a.batch).blocks(a.kv_heads) <= 0x7fffffff;
 }
 
 int64_t attention_workspace_bytes(const AttentionArgs& a) {

@@ -312,13 +312,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool prefix = id < prefix_blocks;
     if (!prefix) id -= prefix_blocks;
     const int splits = prefix ? deal.prefix_splits : deal.own_splits;
-    const int tiles = prefix ? deal.prefix_tiles : deal.own_tiles;
     const int split = (int)(id % splits);
     id /= splits;
     const int h = (int)(id % a.kv_heads);
     id /= a.kv_heads;
-    const int pair = tiles - 1 - (int)(id % tiles);  // the last rows see the most keys: they start first
-    const int b = (int)(id / tiles);                 // own only
+    int pair, b = 0;  // the last rows see the most keys: they start first; b: own only
+    if (prefix) {
+        pair = deal.prefix_tiles - 1 - (int)id;
+    } else if (deal.own_ragged) {
+        griddep_wait();  // before the offsets are read
+        if (!ragged_tile<TILES * BM>(a, deal.own_sets - 1 - id, G, b, pair) ||
+            deal.is_few((int64_t)sequence(a, b).q_len * G))
+            return;
+    } else {
+        pair = deal.own_tiles - 1 - (int)(id % deal.own_tiles);
+        b = (int)(id / deal.own_tiles);
+    }
     const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
     const int base = prefix ? 0 : a.prefix_len;
     const int64_t capacity = prefix ? a.prefix_len : (int64_t)a.max_pages << a.log_page;
@@ -814,7 +823,7 @@ static cudaError_t launch_t(const AttentionArgs& a, const Deal& d, cudaStream_t 
     const int stall = g_stall_next ? 1 : 0;
     g_stall_next = false;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)d.blocks(a.batch, a.kv_heads));
+    cfg.gridDim = dim3((unsigned)d.blocks(a.kv_heads));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Shape<D>::SMEM;
     cfg.stream = s;
