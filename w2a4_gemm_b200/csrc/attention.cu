@@ -108,35 +108,36 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     __shared__ int64_t row_token[R];
     __shared__ int row_pos[R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int G = a.q_heads / a.kv_heads;
+    const uint32_t G = (uint32_t)a.q_heads / (uint32_t)a.kv_heads;
     griddep_wait();
     griddep_launch_dependents();
 
     // ---- which rows and keys
-    int64_t id = blockIdx.x;
-    const int64_t prefix_blocks = (int64_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
+    // Blocks and rows are numbered in 32 bits (the host refuses more): a division of 64 bits takes 100 instructions.
+    uint32_t id = blockIdx.x;
+    const uint32_t prefix_blocks = (uint32_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
     const bool prefix = id < prefix_blocks;
     if (!prefix) id -= prefix_blocks;
-    const int splits = prefix ? deal.prefix_splits : deal.own_splits;
+    const uint32_t splits = prefix ? deal.prefix_splits : deal.own_splits;
     const int split = (int)(id % splits);
     id /= splits;
-    const int h = (int)(id % a.kv_heads);
-    id /= a.kv_heads;
+    const int h = (int)(id % (uint32_t)a.kv_heads);
+    id /= (uint32_t)a.kv_heads;
     int tile, b = 0;  // b: own only
     if (prefix) {
         tile = (int)id;
     } else if (deal.own_ragged) {
         if (!ragged_tile<R>(a, id, G, b, tile)) return;
     } else {
-        tile = (int)(id % deal.own_tiles);
-        b = (int)(id / deal.own_tiles);
+        tile = (int)(id % (uint32_t)deal.own_tiles);
+        b = (int)(id / (uint32_t)deal.own_tiles);
         if (deal.few && !deal.is_few((int64_t)sequence(a, b).q_len * G)) return;
     }
     const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
     const int base = prefix ? 0 : a.prefix_len;
     const int64_t capacity = prefix ? a.prefix_len : (int64_t)a.max_pages << a.log_page;
     if (threadIdx.x < R) {
-        const int64_t r = (int64_t)tile * R + threadIdx.x;
+        const uint32_t r = (uint32_t)tile * R + threadIdx.x;
         int64_t token = -1;
         int pos = -1;
         if (prefix) {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     Range range = {0, 0, 0, 0};
     if (pmax >= 0) range = visible<kStep>(a, pmin, pmax, base, capacity);
     // The host's chunk covers lengths up to its bound; a longer sequence takes longer splits.
-    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
+    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + (int)splits - 1) / (int)splits);
     // The steps, from sure_from on, of which every row sees every key: inside all rows' windows.
     int sure_from = range.head;
     uint32_t sure_steps = 0;
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int64_t token = row_token[8 * n + g];
-        const int head = h * G + (int)(((int64_t)tile * R + 8 * n + g) % G);
+        const int head = (int)(h * G + ((uint32_t)tile * R + 8 * n + g) % G);
         float odd = 0.0f;
 #pragma unroll
         for (int w = 0; w < S::KW; ++w) {
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
     for (int r = warp; r < R; r += kWarps) {
         const int64_t token = row_token[r];
         if (token < 0) continue;
-        const int head = h * G + (int)(((int64_t)tile * R + r) % G);
+        const int head = (int)(h * G + ((uint32_t)tile * R + r) % G);
         float M = kNone, L = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pm[(w * R + r) * 2]);
@@ -491,16 +492,17 @@ __global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stre
 
 // The row-th row to be joined: its token (-1: none), head and number of partial results.  Rows are dealt out as
 // (sequence, token, head), or as (token, head) where that is much less.
-__device__ __forceinline__ int64_t joined_row(const AttentionArgs& a, const Deal& deal, bool by_token, int64_t row, int& head,
+__device__ __forceinline__ int64_t joined_row(const AttentionArgs& a, const Deal& deal, bool by_token, uint32_t row, int& head,
                                               int& slots) {
-    head = (int)(row % a.q_heads);
-    row /= a.q_heads;
-    const int64_t b = by_token ? (row < a.tokens ? sequence_of(a, row) : -1) : row / a.max_q;
+    head = (int)(row % (uint32_t)a.q_heads);
+    row /= (uint32_t)a.q_heads;
+    const int b = by_token ? (row < a.tokens ? sequence_of(a, row) : -1) : (int)(row / (uint32_t)a.max_q);
     if (b < 0 || b >= a.batch) return -1;
-    const Sequence s = sequence(a, (int)b);
-    const int64_t i = by_token ? row - s.first : row % a.max_q;
+    const Sequence s = sequence(a, b);
+    const int64_t i = by_token ? row - s.first : row % (uint32_t)a.max_q;
     if (i < 0 || i >= s.q_len) return -1;
-    slots = deal.prefix_splits + (deal.is_few((int64_t)s.q_len * (a.q_heads / a.kv_heads)) ? deal.few_splits : deal.own_splits);
+    slots = deal.prefix_splits +
+            (deal.few && deal.is_few((int64_t)s.q_len * (a.q_heads / a.kv_heads)) ? deal.few_splits : deal.own_splits);
     return s.first + i;
 }
 
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     int head, slots;
-    const int64_t token = joined_row(a, deal, by_token, (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), head, slots);
+    const int64_t token = joined_row(a, deal, by_token, blockIdx.x * 8 + (threadIdx.x >> 5), head, slots);
     if (token < 0) return;
     const Parts p = parts(a, deal.slots);
     const int64_t at = (token * a.q_heads + head) * deal.slots;

@@ -68,7 +68,7 @@ __device__ __forceinline__ Sequence sequence(const AttentionArgs& a, int b) {
 
 // The sequence a token belongs to, -1 if none: the last b with cu_q[b] <= token < cu_q[b + 1].
 __device__ __forceinline__ int sequence_of(const AttentionArgs& a, int64_t token) {
-    if (!a.cu_q) return (int)(token / a.max_q);
+    if (!a.cu_q) return (int)((uint32_t)token / (uint32_t)a.max_q);
     int lo = 0, hi = a.batch;  // first b in [lo, hi] with cu_q[b] > token
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -125,7 +125,7 @@ __device__ __forceinline__ Range visible(const AttentionArgs& a, int pmin, int p
 // one's whatever the lengths are, and for all of them in tokens * G / PER + batch.  (A tile for each PER of
 // the longest sequence's rows, of every sequence, would be mostly empty.)  False: no rows.
 template <int PER>
-__device__ __forceinline__ bool ragged_tile(const AttentionArgs& a, int64_t x, int G, int& b, int& tile) {
+__device__ __forceinline__ bool ragged_tile(const AttentionArgs& a, int64_t x, uint32_t G, int& b, int& tile) {
     auto start = [&](int s) {
         int64_t first = a.cu_q[s];
         first = first < 0 ? 0 : first > a.tokens ? a.tokens : first;

@@ -304,18 +304,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* gone = reinterpret_cast<uint32_t*>(most + RING);           // [RING] 16s of keys that are not there
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in all lanes
-    const int G = a.q_heads / a.kv_heads;
+    const uint32_t G = (uint32_t)a.q_heads / (uint32_t)a.kv_heads;
 
     // ---- which rows and keys
-    int64_t id = blockIdx.x;
-    const int64_t prefix_blocks = (int64_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
+    // Blocks and rows are numbered in 32 bits (the host refuses more): a division of 64 bits takes 100 instructions.
+    uint32_t id = blockIdx.x;
+    const uint32_t prefix_blocks = (uint32_t)a.kv_heads * deal.prefix_tiles * deal.prefix_splits;
     const bool prefix = id < prefix_blocks;
     if (!prefix) id -= prefix_blocks;
-    const int splits = prefix ? deal.prefix_splits : deal.own_splits;
+    const uint32_t splits = prefix ? deal.prefix_splits : deal.own_splits;
     const int split = (int)(id % splits);
     id /= splits;
-    const int h = (int)(id % a.kv_heads);
-    id /= a.kv_heads;
+    const int h = (int)(id % (uint32_t)a.kv_heads);
+    id /= (uint32_t)a.kv_heads;
     int pair, b = 0;  // the last rows see the most keys: they start first; b: own only
     if (prefix) {
         pair = deal.prefix_tiles - 1 - (int)id;
@@ -325,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             deal.is_few((int64_t)sequence(a, b).q_len * G))
             return;
     } else {
-        pair = deal.own_tiles - 1 - (int)(id % deal.own_tiles);
-        b = (int)(id / deal.own_tiles);
+        pair = deal.own_tiles - 1 - (int)(id % (uint32_t)deal.own_tiles);
+        b = (int)(id / (uint32_t)deal.own_tiles);
     }
     const int32_t* table = prefix ? a.prefix_table : a.page_table + (int64_t)b * a.max_pages;
     const int base = prefix ? 0 : a.prefix_len;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t token = -1;
     int pos = -1, head = 0;
     if (warp < kSoftWarps) {
-        const int64_t row = ((int64_t)pair * TILES + tile) * BM + r;
+        const uint32_t row = (uint32_t)(pair * TILES + tile) * BM + r;
         if (prefix) {
             if (row < a.tokens * G) token = row / G, pos = position_of(a, token);
             if (pos < -1) token = pos = -1;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (token >= a.tokens || token < 0) token = -1;
-        head = h * G + (int)(row % G);
+        head = (int)(h * G + row % G);
         if (token >= 0) {
             atomicMin(&bar.least[tile], pos);
             if (pos >= 0) atomicMin(&bar.pmin[tile], pos), atomicMax(&bar.pmax[tile], pos);
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pmax = max(bar.pmax[0], bar.pmax[1]);
     Range range = {0, 0, 0, 0};
     if (pmax >= 0) range = visible<BN>(a, min(bar.pmin[0], bar.pmin[1]), pmax, base, capacity);
-    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + splits - 1) / splits);
+    const int chunk = max(prefix ? deal.prefix_chunk : deal.own_chunk, (range.steps + (int)splits - 1) / (int)splits);
     const int s_begin = min(split * chunk, range.steps), n = min(chunk, range.steps - s_begin);
     const int shift = range.main - range.head;
     auto block_of = [&](int i) { return s_begin + i + (s_begin + i >= range.head ? shift : 0); };
