@@ -637,9 +637,10 @@ struct Cut {
 // streaming kernel (`per` rows a block) or the one for many rows.
 // Streaming: a split is at least 512 keys (four steps a warp) and, of a batch of unequal lengths, at most 4096.
 // Rows of equal lengths are split into one turn of the GPU (four blocks an SM): 131071 keys by 8 kv heads
-// took 42 us, with two turns 52 and with four 77.  Unequal ones into two turns, counted by the bound on their
-// lengths, so that short ones leave no gap: 64 sequences of 8000-16384 keys took 197 us with one turn, 179
-// with two and 174 with four.
+// take 37 us, with two turns 42; 33 windows of 4096 keys by 8 27.3 and 29.7.  Unequal ones into three turns, counted by
+// the bound on their lengths, so that short ones leave no gap: 16 sequences of 300-4096 keys by 32 kv heads take
+// 45.1 us with three turns, 46.7 with one or two, 46.6 with four and 50.6 with six; 64 of 8000-16384 by 8
+// the same, 165 us, with any of them.
 // Many rows: one block an SM, split only where there are fewer row sets than SMs.
 static Cut cut(bool wide, int per, int64_t kv_heads, int64_t batch, int64_t rows, int64_t all_rows, int64_t keys, bool equal,
                int head_dim) {
@@ -653,7 +654,7 @@ static Cut cut(bool wide, int per, int64_t kv_heads, int64_t batch, int64_t rows
     c.ragged = 2 * total <= c.sets;                // a search through the offsets, for half of the blocks
     if (c.ragged) c.sets = total;
     const int64_t blocks = kv_heads * c.sets;
-    int64_t n = wide ? 148 / blocks : (equal ? 1 : 2) * 592 / blocks;
+    int64_t n = wide ? 148 / blocks : (equal ? 1 : 3) * 592 / blocks;
     n = std::max<int64_t>(std::max<int64_t>(1, (steps + most - 1) / most), std::min(n, steps / least));
     n = std::min<int64_t>(n, kMostSlots / 2);
     c.chunk = (int)((steps + n - 1) / n);
