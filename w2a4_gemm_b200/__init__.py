@@ -358,6 +358,7 @@ def qift_decode_linear(x: torch.Tensor, block: int, codes: torch.Tensor, w_scale
 # tensor, and the checks above only to say what is wrong.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_U8, _F16, _F32, _I32, _I64 = torch.uint8, torch.float16, torch.float32, torch.int32, torch.int64
 
 
 def _is(t, name: str, dtype, shape: tuple, index: int) -> int:
@@ -372,33 +373,49 @@ def _is(t, name: str, dtype, shape: tuple, index: int) -> int:
 def _heads(t, name: str, shape: tuple, index: int) -> tuple[int, int]:
     """Address and elements between tokens of a [tokens, heads, head_dim] fp16 tensor whose heads lie one behind
     the other (a slice of a projection's output is one)."""
+    n, h, d = shape
+    if isinstance(t, torch.Tensor) and t.dtype is _F16 and t.shape == shape and t.get_device() == index:
+        row, head, one = t.stride()
+        if n <= 1:
+            row = h * d
+        if (one == 1 or d <= 1) and (head == d or h <= 1) and row >= h * d:
+            return t.data_ptr(), row
+        raise ValueError(f"{name} must hold each token's heads one behind the other, got strides {t.stride()}")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.dtype is not torch.float16:
+    if t.dtype is not _F16:
         raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{index}")
-    n, h, d = shape
-    row, head, one = t.stride()
-    if n <= 1:
-        row = h * d
-    if (one != 1 and d > 1) or (head != d and h > 1) or row < h * d:
-        raise ValueError(f"{name} must hold each token's heads one behind the other, got strides {t.stride()}")
-    return t.data_ptr(), row
+    _shape(t, name, shape)
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{index}")
 
 
 def _cache(k_cache, k_scales, v_cache, v_scales):
-    """Checks a paged cache; returns its addresses, (pages, kv_heads, page_size, head_dim) and its device's index."""
-    _cuda(k_cache, "k_cache", torch.uint8)
+    """Checks a paged cache; returns its addresses, pages, kv_heads, page_size, head_dim and its device's index."""
+    _cuda(k_cache, "k_cache", _U8)
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim / 2], got shape {tuple(shape)}")
-    index, of_scales = k_cache.get_device(), shape[:3]
-    at = (k_cache.data_ptr(), _is(k_scales, "k_scales", torch.float32, of_scales, index),
-          _is(v_cache, "v_cache", torch.uint8, shape, index), _is(v_scales, "v_scales", torch.float32, of_scales, index))
-    return at, (shape[0], shape[1], shape[2], 2 * shape[3]), index
+    pages, kv_heads, size, half = shape
+    rows, index = (pages, kv_heads, size), k_cache.get_device()
+    return (k_cache.data_ptr(), _is(k_scales, "k_scales", _F32, rows, index), _is(v_cache, "v_cache", _U8, shape, index),
+            _is(v_scales, "v_scales", _F32, rows, index), pages, kv_heads, size, 2 * half, index)
+
+
+def _on(stream, index: int):
+    """The stream to launch on: `stream`, or the current one of device `index`."""
+    if stream is None:
+        return _current_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _launch(index: int, fn, args: tuple) -> int:
+    """Calls the library's `fn` with device `index` current."""
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _int32(**values):
@@ -406,20 +423,6 @@ def _int32(**values):
     for name, x in values.items():
         if not -2 ** 31 <= x < 2 ** 31:
             raise ValueError(f"{name} must fit 32 bits, got {x}")
-
-
-def _launch(index: int, stream, fn, *args) -> int:
-    """Calls the library's `fn` on `stream` (None: the current one of device `index`) with that device current."""
-    if stream is None:
-        stream = _current_stream(index)
-    elif stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
-    else:
-        stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        return fn(*args, stream)
-    with torch.cuda.device(index):
-        return fn(*args, stream)
 
 
 def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block: int, k_cache: torch.Tensor,
@@ -434,36 +437,42 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
     fp32 ``[pages, kv_heads, page_size]`` are written at ``slots`` (int64, ``page * page_size + offset``; -1 =
     padding).  ``rope`` fp32 ``[positions, rope_dim]`` holds cosines, then sines, and ``positions`` (int64) its row
     for each token.  Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
-    _int32(block=block)
-    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    if not 0 <= block < 2 ** 31:
+        _int32(block=block)
+    kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
-    k_at, k_row = _heads(k, "k", (T, kv_heads, d), index)
-    v_at, v_row = _heads(v, "v", (T, kv_heads, d), index)
-    slots_at = _is(slots, "slots", torch.int64, (T,), index)
+    rows = (T, kv_heads, d)
+    k_at, k_row = _heads(k, "k", rows, index)
+    v_at, v_row = _heads(v, "v", rows, index)
+    slots_at = _is(slots, "slots", _I64, (T,), index)
     q_at = out_at = rope_at = positions_at = None
     q_row = hq = rope_len = rope_dim = 0
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        rope_len, rope_dim = _2d(_cuda(rope, "rope", torch.float32), "rope").shape
-        rope_at = _is(rope, "rope", torch.float32, (rope_len, rope_dim), index)
-        positions_at = _is(positions, "positions", torch.int64, (T,), index)
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            _2d(_cuda(rope, "rope", _F32), "rope")
+        rope_len, rope_dim = shape = rope.shape
+        rope_at = _is(rope, "rope", _F32, shape, index)
+        positions_at = _is(positions, "positions", _I64, (T,), index)
     if q is not None:
         hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
         q_at, q_row = _heads(q, "q", (T, hq, d), index)
         if hq == 0:
             raise ValueError("q must have at least one head")
         if q_out is None:
-            q_out = q.new_empty((T, hq, d))
+            q_out = torch.empty_like(q) if T <= 1 or q_row == hq * d else q.new_empty((T, hq, d))
             out_at = q_out.data_ptr()
         else:
-            out_at = _is(q_out, "q_out", torch.float16, (T, hq, d), index)
+            out_at = _is(q_out, "q_out", _F16, (T, hq, d), index)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if T:  # an empty tensor has no address
-        _check(_launch(index, stream, lib().qift_append_kv, q_at, q_row, k_at, k_row, v_at, v_row, T, hq, kv_heads, d,
-                       rope_at, rope_len, rope_dim, 1 if interleaved else 0, positions_at, slots_at, block, out_at, kc,
-                       ks, vc, vs, pages, size), "qift_append_kv")
+        status = _launch(index, (_lib or lib()).qift_append_kv, (
+            q_at, q_row, k_at, k_row, v_at, v_row, T, hq, kv_heads, d, rope_at, rope_len, rope_dim, 1 if interleaved else 0,
+            positions_at, slots_at, block, out_at, kc, ks, vc, vs, pages, size, _on(stream, index)))
+        if status:
+            _check(status, "qift_append_kv")
     return q_out
 
 
@@ -471,14 +480,17 @@ def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch
                    slots: torch.Tensor, block: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Rows of a paged KV4 cache read back, rotated back by ``block`` (0: in the cache's domain): fp16
     ``(k, v)``, each ``[tokens, kv_heads, head_dim]``; zeros for slots outside the cache."""
-    _int32(block=block)
-    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    if not 0 <= block < 2 ** 31:
+        _int32(block=block)
+    kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() else 0
-    slots_at = _is(slots, "slots", torch.int64, (T,), index)
-    k = k_scales.new_empty((T, kv_heads, d), dtype=torch.float16)
+    slots_at = _is(slots, "slots", _I64, (T,), index)
+    k = k_scales.new_empty((T, kv_heads, d), dtype=_F16)
     v = torch.empty_like(k)
-    _check(_launch(index, stream, lib().qift_gather_kv, kc, ks, vc, vs, pages, size, kv_heads, d, slots_at, T, block,
-                   k.data_ptr(), v.data_ptr()), "qift_gather_kv")
+    status = _launch(index, (_lib or lib()).qift_gather_kv, (
+        kc, ks, vc, vs, pages, size, kv_heads, d, slots_at, T, block, k.data_ptr(), v.data_ptr(), _on(stream, index)))
+    if status:
+        _check(status, "qift_gather_kv")
     return k, v
 
 
@@ -502,7 +514,7 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     that belong to no sequence are not initialised."""
     if not 0 <= (max_q | window | sinks | prefix_len | max_kv | block) < 2 ** 31:
         _int32(max_q=max_q, window=window, sinks=sinks, prefix_len=prefix_len, max_kv=max_kv, block=block)
-    (kc, ks, vc, vs), (pages, kv_heads, size, d), index = _cache(k_cache, k_scales, v_cache, v_scales)
+    kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [tokens, q_heads, head_dim] tensor")
     shape = q.shape
@@ -511,27 +523,27 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [batch, max_pages] tensor")
     B, max_pages = table_shape = page_table.shape
-    table_at = _is(page_table, "page_table", torch.int32, table_shape, index)
-    lens_at = _is(kv_lens, "kv_lens", torch.int32, (B,), index)
+    table_at = _is(page_table, "page_table", _I32, table_shape, index)
+    lens_at = _is(kv_lens, "kv_lens", _I32, (B,), index)
     cu_at = prefix_at = lse_at = None
     if cu_q is not None:
-        cu_at = _is(cu_q, "cu_q", torch.int32, (B + 1,), index)
+        cu_at = _is(cu_q, "cu_q", _I32, (B + 1,), index)
     elif T != B * max_q:
         raise ValueError(f"without cu_q, q must have batch * max_q = {B * max_q} rows, got {T}")
     if prefix_table is not None:
-        _at_least(_cuda(prefix_table, "prefix_table", torch.int32), "prefix_table", -(-prefix_len // size))
-        prefix_at = _is(prefix_table, "prefix_table", torch.int32, prefix_table.shape, index)
+        _at_least(_cuda(prefix_table, "prefix_table", _I32), "prefix_table", -(-prefix_len // size))
+        prefix_at = _is(prefix_table, "prefix_table", _I32, prefix_table.shape, index)
     elif prefix_len != 0:
         raise ValueError("prefix_len needs prefix_table")
-    if out_dtype is not torch.float16 and out_dtype is not torch.float32:
+    if out_dtype is not _F16 and out_dtype is not _F32:
         raise ValueError("out_dtype must be torch.float16 or torch.float32")
     if lse is not None:
         lse_at = _is(lse, "lse", torch.float32, (T, hq), index)
     need = _workspace_bytes(T, hq, kv_heads, d, B, max_q, size, max_pages, max_kv, prefix_len, window, sinks)
     ws_at, ws_bytes = None, 0
     if workspace is not None:
-        _at_least(_cuda(workspace, "workspace", torch.uint8), "workspace", need)
-        ws_at, ws_bytes = _is(workspace, "workspace", torch.uint8, workspace.shape, index), workspace.numel()
+        _at_least(_cuda(workspace, "workspace", _U8), "workspace", need)
+        ws_at, ws_bytes = _is(workspace, "workspace", _U8, workspace.shape, index), workspace.numel()
     elif need > 0:
         if stream is None:
             workspace = k_cache.new_empty(need)
@@ -540,15 +552,17 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
                 workspace = k_cache.new_empty(need)
         ws_at, ws_bytes = workspace.data_ptr(), need
     if out is None:
-        out = torch.empty_like(q) if out_dtype is torch.float16 and q.is_contiguous() else q.new_empty(shape, dtype=out_dtype)
+        plain = out_dtype is _F16 and (T <= 1 or q_row == hq * d)
+        out = torch.empty_like(q) if plain else q.new_empty(shape, dtype=out_dtype)
         out_at = out.data_ptr()
     else:
         out_at = _is(out, "out", out_dtype, shape, index)
-    _check(_launch(index, stream, lib().qift_paged_attention, q_at, q_row, T, hq, kv_heads, d, cu_at, B, max_q, kc, ks,
-                   vc, vs, pages, size, table_at, max_pages, lens_at, max_kv, prefix_at, prefix_len, window, sinks,
-                   1.0 / math.sqrt(d) if scale is None else scale, block, out_at,
-                   QIFT_F16 if out_dtype is torch.float16 else QIFT_F32, lse_at, ws_at, ws_bytes),
-           "qift_paged_attention")
+    status = _launch(index, (_lib or lib()).qift_paged_attention, (
+        q_at, q_row, T, hq, kv_heads, d, cu_at, B, max_q, kc, ks, vc, vs, pages, size, table_at, max_pages, lens_at, max_kv,
+        prefix_at, prefix_len, window, sinks, 1.0 / math.sqrt(d) if scale is None else scale, block, out_at,
+        QIFT_F16 if out_dtype is _F16 else QIFT_F32, lse_at, ws_at, ws_bytes, _on(stream, index)))
+    if status:
+        _check(status, "qift_paged_attention")
     return out
 
 
