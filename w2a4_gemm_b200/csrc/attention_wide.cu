@@ -11,8 +11,8 @@
 // whole numbers in binary16 in the layout the tensor core reads: K rows of keys, V transposed (rows of
 // values, so that both operands are contiguous along the sum), 128-byte swizzled.  The scales are applied
 // in fp32 to S and to the weights, so the one rounding is that of p.  (Folded into the binary16 operands
-// instead, scales cost nothing in the softmax and the prompt of 8192 tokens took 598 us for 614, but the
-// result's error was 5.5e-4 for 2.9e-4.)  The order of values inside each group of eight is that in which a
+// instead, scales cost nothing in the softmax and the prompt of 8192 tokens took 16 us less of 614, but the
+// result's error was 5.5e-4 for 2.7e-4.)  The order of values inside each group of eight is that in which a
 // word's nibbles come out; Q is laid out alike.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has a row
@@ -24,8 +24,8 @@
 // A row's reference is raised (and O scaled down) only when the weights of a half step might not fit
 // binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j.
 //
-// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 614 us, 56% of the
-// measured bf16 matrix rate over the visible half): a step of 256 rows by 128 keys takes about 4000 cycles.
+// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 587 us, 58% of the
+// measured bf16 matrix rate over the visible half, 610 us in a long run under the power limit): a step of 256 rows by 128 keys takes about 4000 cycles.
 // S in halves of 64 keys costs the tensor core about 90 cycles a product, half of its rate, since Q is read
 // from shared memory for each; P V 64; together some 3300.  The exponentials of 256 x 128 weights take the
 // special-function unit 2048.  Exponentials on the fp32 pipe (a polynomial for a quarter to a half of the
