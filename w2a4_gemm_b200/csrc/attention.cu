@@ -659,7 +659,7 @@ static Cut cut(bool wide, int per, int64_t kv_heads, int64_t batch, int64_t rows
     c.tiles = (int)((rows + per - 1) / per);
     c.sets = batch * c.tiles;
     const int64_t total = all_rows / per + batch;  // never less than the tiles of equal sets
-    c.ragged = 2 * total <= c.sets;                // a search through the offsets, for half of the blocks
+    c.ragged = total < c.sets;  // an empty block of the kernel for many rows took 7 us, a search through the offsets 1
     if (c.ragged) c.sets = total;
     const int64_t blocks = kv_heads * c.sets;
     int64_t n = wide ? 148 / blocks : (equal ? 1 : 3) * 592 / blocks;
@@ -707,7 +707,7 @@ static Deal deal_out(const AttentionArgs& a) {
     } else if (a.head_dim <= 128 && pin == kAttentionAuto) {
         const Cut many = own_cut(true, 0), few = own_cut(false, 16);
         d.own_wide = own_rows > 16 && many.us < few.us;
-        if (own_rows > 16 && G <= 16 && many.ragged) {
+        if (own_rows > 16 && G <= 16 && 2 * many.sets <= (int64_t)a.batch * many.tiles) {
             // Long sequences among short ones (prompts among single tokens): each to its kernel, if one long
             // sequence with all the rows and single tokens of the others would be faster so.  Blocks of the
             // kernel for many rows that find a short sequence leave at once (about 1 us of an SM).

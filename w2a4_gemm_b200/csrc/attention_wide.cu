@@ -387,10 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (token >= a.tokens || token < 0) token = -1;
         head = (int)(h * G + row % G);
-        if (token >= 0) {
-            atomicMin(&bar.least[tile], pos);
-            if (pos >= 0) atomicMin(&bar.pmin[tile], pos), atomicMax(&bar.pmax[tile], pos);
-        }
+        const int least = __reduce_min_sync(0xffffffffu, token >= 0 ? pos : 0x7fffffff);
+        const int pmin = __reduce_min_sync(0xffffffffu, token >= 0 && pos >= 0 ? pos : 0x7fffffff);
+        const int pmax = __reduce_max_sync(0xffffffffu, token >= 0 ? pos : -1);
+        if (lane == 0) atomicMin(&bar.least[tile], least), atomicMin(&bar.pmin[tile], pmin), atomicMax(&bar.pmax[tile], pmax);
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int block = finish ? a.block : 0;
             const float by = (finish ? (sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum)) : 1.0f) *
                              (block ? a.norm : 1.0f);
+            const uint64_t by2 = pack2(by, by), minus = pack2(-1.0f, -1.0f);
             int64_t at = token >= 0 ? token * a.q_heads + head : -1;
             if (finish) {
                 if (a.lse && token >= 0) a.lse[at] = sum == 0.0f ? -INFINITY : 0.69314718056f * (ref + log2f(sum));
@@ -522,45 +523,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_ld_32x32b_x32(t_o + 32 * c, x);
                     tmem_ld_wait_for(x);
                 }
-                float v[32];
+                uint64_t v[16];  // two values at a time; x - y as x + (-1) y, exactly the same
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(x[e]) * by;
+                for (int e = 0; e < 16; ++e) v[e] = mul2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), by2);
+                if (block > 1) {
 #pragma unroll
-                for (int hd = 1; hd < 32; hd <<= 1) {
-                    if (block > hd) {
+                    for (int e = 0; e < 16; ++e) {
+                        float y, z;
+                        unpack2(v[e], y, z);
+                        v[e] = pack2(y + z, y - z);
+                    }
+                }
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                for (int hd = 1; hd < 16; hd <<= 1) {
+                    if (block > 2 * hd) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
                             if (e & hd) continue;
-                            const float y = v[e], z = v[e + hd];
-                            v[e] = y + z;
-                            v[e + hd] = y - z;
+                            const uint64_t y = v[e], z = v[e + hd];
+                            v[e] = add2(y, z);
+                            v[e + hd] = fma2(z, minus, y);
                         }
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(mine + 32 * c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                for (int e = 0; e < 16; e += 2) *reinterpret_cast<ulonglong2*>(mine + 32 * c + 2 * e) = make_ulonglong2(v[e], v[e + 1]);
             }
             if (block > 32) {
-#pragma unroll 1
+#pragma unroll 2
                 for (int e = 0; e < 32; e += 4) {
-                    float4 v[D / 32];
+                    ulonglong2 v[D / 32];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) v[c] = *reinterpret_cast<const float4*>(mine + 32 * c + e);
+                    for (int c = 0; c < D / 32; ++c) v[c] = *reinterpret_cast<const ulonglong2*>(mine + 32 * c + e);
 #pragma unroll
                     for (int hd = 1; hd < D / 32; hd <<= 1) {
                         if (block > 32 * hd) {
 #pragma unroll
                             for (int c = 0; c < D / 32; ++c) {
                                 if (c & hd) continue;
-                                const float4 y = v[c], z = v[c + hd];
-                                v[c] = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
-                                v[c + hd] = make_float4(y.x - z.x, y.y - z.y, y.z - z.z, y.w - z.w);
+                                const ulonglong2 y = v[c], z = v[c + hd];
+                                v[c] = make_ulonglong2(add2(y.x, z.x), add2(y.y, z.y));
+                                v[c + hd] = make_ulonglong2(fma2(z.x, minus, y.x), fma2(z.y, minus, y.y));
                             }
                         }
                     }
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) *reinterpret_cast<float4*>(mine + 32 * c + e) = v[c];
+                    for (int c = 0; c < D / 32; ++c) *reinterpret_cast<ulonglong2*>(mine + 32 * c + e) = v[c];
                 }
             }
             __syncwarp();
