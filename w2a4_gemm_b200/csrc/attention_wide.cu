@@ -24,9 +24,9 @@
 // A row's reference is raised (and O scaled down) only when the weights of a half step might not fit
 // binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j.
 //
-// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 587 us, 58% of the
-// measured bf16 matrix rate over the visible half, 610 us in a long run under the power limit): a step of 256 rows by 128 keys takes about 4000 cycles.
-// S in halves of 64 keys costs the tensor core about 90 cycles a product, half of its rate, since Q is read
+// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 581 us, 59% of the
+// measured bf16 matrix rate over the visible half, 614 us in a long run under the power limit): a step of 256
+// rows by 128 keys takes 4000 to 4400 cycles.  S in halves of 64 keys costs the tensor core about 90 cycles a product, half of its rate, since Q is read
 // from shared memory for each; P V 64; together some 3300.  The exponentials of 256 x 128 weights take the
 // special-function unit 2048.  Exponentials on the fp32 pipe (a polynomial for a quarter to a half of the
 // weights) made it slower (690-740 us): the softmax waits for latency, not for that unit.
