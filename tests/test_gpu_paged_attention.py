@@ -684,3 +684,95 @@ def test_the_choice_of_kernel_is_by_cost():
     auto = call(one)
     qg.qift_debug_set_attention_path("stream")
     assert torch.equal(auto, call(one))
+
+
+# ------------------------------------------------------------------------------- as a server would call them
+def test_a_captured_step_follows_lengths_slots_and_positions():
+    """One graph of append and attention, replayed for step after step of a batch whose members differ in length
+    and in the number of new tokens, on a stream of its own while another graph of the same kind runs beside it."""
+    hq, hk, d, size, B, T = 8, 2, 128, 16, 4, 60
+    tab = rope_table(4096, d).cuda()
+    def batch(seed):
+        g = gen(seed)
+        s = dict(qkv=torch.randn(T, hq + 2 * hk, d, device="cuda", generator=g).half(), cache=empty_cache(B * 12, hk, size, d),
+                 table=torch.randperm(B * 12, device="cuda", generator=g).to(torch.int32).view(B, 12),
+                 cu=torch.zeros(B + 1, dtype=torch.int32, device="cuda"), lens=torch.zeros(B, dtype=torch.int32, device="cuda"),
+                 slots=torch.full((T,), -1, device="cuda"), positions=torch.zeros(T, dtype=torch.int64, device="cuda"))
+        return s
+    def step(s, cache):
+        q = qg.qift_append_kv(s["qkv"][:, hq:hq + hk], s["qkv"][:, hq + hk:], s["slots"], d, *cache, q=s["qkv"][:, :hq],
+                              positions=s["positions"], rope=tab)
+        return qg.qift_paged_attention(q, s["cu"], 40, *cache, s["table"], s["lens"], block=d)
+    def advance(s, counts, at):
+        table = s["table"].cpu()
+        slots, positions = [], []
+        for b, n in enumerate(counts):
+            for i in range(n):
+                p = at[b] + i
+                slots.append(int(table[b, p // size]) * size + p % size)
+                positions.append(p)
+            at[b] += n
+        pad = T - len(slots)
+        s["slots"].copy_(torch.tensor(slots + [-1] * pad))
+        s["positions"].copy_(torch.tensor(positions + [0] * pad))
+        s["cu"].copy_(torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32))
+        s["lens"].copy_(torch.tensor(at, dtype=torch.int32))
+        return len(slots)
+    batches, streams, graphs, outs = [batch(1), batch(2)], [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for s, stream in zip(batches, streams):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step(s, s["cache"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs.append(step(s, s["cache"]))
+        graphs.append(graph)
+    eager = [[c.clone() for c in s["cache"]] for s in batches]
+    at = [[0] * B, [0] * B]
+    for counts in ([40, 1, 3, 0], [1, 1, 1, 1], [1, 0, 40, 1], [2, 30, 1, 1], [1, 1, 1, 1]):
+        used = [advance(s, c, a) for s, c, a in zip(batches, (counts, counts[::-1]), at)]
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for s, cache, out, n in zip(batches, eager, outs, used):
+            want = step(s, cache)
+            assert torch.equal(out[:n], want[:n]) and not torch.isnan(out[:n]).any()
+            for x, y in zip(s["cache"], cache):
+                assert torch.equal(torch.nan_to_num(x.float(), 5e4), torch.nan_to_num(y.float(), 5e4))
+
+
+def test_tokens_whose_elements_pass_32_bits():
+    T, hq, hk, d, last = 600_000, 32, 8, 128, 50  # 3.7e9 elements in, 2.5e9 out
+    g = gen(4)
+    qkv = torch.zeros(T, hq + 2 * hk, d, dtype=torch.float16, device="cuda")
+    qkv[-last:] = torch.randn(last, hq + 2 * hk, d, device="cuda", generator=g).half()
+    slots = torch.full((T,), -1, device="cuda")
+    slots[-last:] = torch.arange(last, device="cuda") * 16
+    big, small = empty_cache(last, hk, 16, d), empty_cache(last, hk, 16, d)
+    q = qg.qift_append_kv(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, d, *big, q=qkv[:, :hq])
+    tail = qkv[-last:].clone()
+    del qkv
+    few = qg.qift_append_kv(tail[:, hq:hq + hk], tail[:, hq + hk:], slots[-last:].clone(), d, *small, q=tail[:, :hq])
+    assert torch.equal(q[-last:], few)
+    for x, y in zip(big, small):
+        assert torch.equal(torch.nan_to_num(x.float(), 5e4), torch.nan_to_num(y.float(), 5e4))
+    # every token a sequence of one key, so that its result is that key's value; the last ones have one each
+    table = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    table[-last:, 0] = torch.arange(last, dtype=torch.int32, device="cuda")
+    lens = torch.ones(T, dtype=torch.int32, device="cuda")
+    lse = torch.empty(T, hq, device="cuda")
+    out = qg.qift_paged_attention(q, None, 1, *big, table, lens, lse=lse)
+    _, v = qg.qift_gather_kv(*big, slots[-last:].clone(), 0)
+    want = v.repeat_interleave(hq // hk, 1).float()
+    assert ((out[-last:].float() - want).abs() <= want.abs() * (2.0 ** -11 * 3 + 2.0 ** -17)).all()  # the weight, and either result's rounding
+    assert (out[0].float() - want[0]).abs().amax() <= want[0].abs().amax() * 2.0 ** -9
+    k, _ = qg.qift_gather_kv(*big, slots[-last:].clone(), 0)
+    u = (q[-last:].double() * k.repeat_interleave(hq // hk, 1).double()).sum(-1) / math.sqrt(d)
+    # k read back is rounded to binary16: half a step, 2^-11, of each of its values
+    reach = (q[-last:].double() * k.repeat_interleave(hq // hk, 1).double()).abs().sum(-1) / math.sqrt(d)
+    s_max = small[1].nan_to_num(0.0).amax()
+    e_u = score_error(q[-last:].double().abs().sum(-1) * s_max / math.sqrt(d), d)
+    assert ((lse[-last:].double() - u).abs() <= reach * 2.0 ** -11 + e_u + 2.0 ** -16 + u.abs() * 2.0 ** -20).all()
