@@ -358,6 +358,7 @@ def qift_decode_linear(x: torch.Tensor, block: int, codes: torch.Tensor, w_scale
 # tensor, and the checks above only to say what is wrong.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # tensors exist: CUDA is up
 _U8, _F16, _F32, _I32, _I64 = torch.uint8, torch.float16, torch.float32, torch.int32, torch.int64
 
 
@@ -391,7 +392,18 @@ def _heads(t, name: str, shape: tuple, index: int) -> tuple[int, int]:
 
 def _cache(k_cache, k_scales, v_cache, v_scales):
     """Checks a paged cache; returns its addresses, pages, kv_heads, page_size, head_dim and its device's index."""
-    _cuda(k_cache, "k_cache", _U8)
+    try:
+        pages, kv_heads, size, half = shape = k_cache.shape
+        rows, index = (pages, kv_heads, size), k_cache.get_device()
+        if index >= 0 and k_cache.dtype is _U8 and v_cache.dtype is _U8 and k_scales.dtype is _F32 and \
+                v_scales.dtype is _F32 and v_cache.shape == shape and k_scales.shape == rows and v_scales.shape == rows and \
+                v_cache.get_device() == k_scales.get_device() == v_scales.get_device() == index and \
+                k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous():
+            return (k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(), v_scales.data_ptr(), pages, kv_heads, size,
+                    2 * half, index)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _cuda(k_cache, "k_cache", _U8)  # which of it
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError(f"k_cache must be [pages, kv_heads, page_size, head_dim / 2], got shape {tuple(shape)}")
@@ -412,7 +424,7 @@ def _on(stream, index: int):
 
 def _launch(index: int, fn, args: tuple) -> int:
     """Calls the library's `fn` with device `index` current."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)

@@ -44,9 +44,9 @@ int log2_of(int32_t v) {
     return l;
 }
 
-// Sizes of an attention call; `a` receives them.
-qift_status attention_sizes(qift::AttentionArgs* a, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                            int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages, int32_t max_kv,
+// Sizes of an attention call; `a` receives them, `deal` how its work is dealt out.
+qift_status attention_sizes(qift::AttentionArgs* a, qift::attn::Deal* deal, int64_t tokens, int32_t q_heads,
+                            int32_t kv_heads, int32_t head_dim, int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages, int32_t max_kv,
                             int32_t prefix_len, int32_t window, int32_t sinks) {
     const qift_status st = cache_shape(0, page_size, kv_heads, head_dim);
     if (st != QIFT_OK) return st;
@@ -67,7 +67,7 @@ qift_status attention_sizes(qift::AttentionArgs* a, int64_t tokens, int32_t q_he
     a->prefix_len = prefix_len;
     a->window = window;
     a->sinks = sinks;
-    if (tokens > 0 && batch > 0 && max_q > 0 && !qift::attention_supported(*a)) return QIFT_ERR_UNSUPPORTED;
+    if (tokens > 0 && batch > 0 && max_q > 0 && !qift::plan_attention(*a, deal)) return QIFT_ERR_UNSUPPORTED;
     return QIFT_OK;
 }
 
@@ -401,10 +401,11 @@ int64_t qift_paged_attention_workspace(int64_t tokens, int32_t q_heads, int32_t 
                                        int32_t batch, int32_t max_q, int32_t page_size, int32_t max_pages,
                                        int32_t max_kv, int32_t prefix_len, int32_t window, int32_t sinks) {
     qift::AttentionArgs a = {};
-    if (attention_sizes(&a, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv, prefix_len,
+    qift::attn::Deal deal = {};
+    if (attention_sizes(&a, &deal, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv, prefix_len,
                         window, sinks) != QIFT_OK)
         return -1;
-    return tokens == 0 || batch == 0 || max_q == 0 ? 0 : qift::attention_workspace_bytes(a);
+    return tokens == 0 || batch == 0 || max_q == 0 ? 0 : qift::attention_workspace_bytes(a, deal);
 }
 
 qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens, int32_t q_heads, int32_t kv_heads,
@@ -419,7 +420,8 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
     qift_status st = cache_shape(n_pages, page_size, kv_heads, head_dim);
     if (st != QIFT_OK) return st;
     qift::AttentionArgs a = {};
-    st = attention_sizes(&a, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv,
+    qift::attn::Deal deal = {};
+    st = attention_sizes(&a, &deal, tokens, q_heads, kv_heads, head_dim, batch, max_q, page_size, max_pages, max_kv,
                          prefix_len, window, sinks);
     if (st != QIFT_OK) return st;
     if (!head_block(block, head_dim) || !isfinite(scale)) return QIFT_ERR_INVALID_ARG;
@@ -437,7 +439,7 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
     const int64_t row = (int64_t)q_heads * head_dim;  // a block reads its queries while another may have written its rows
     if (overlap(out, tokens * row * (out_dt == QIFT_F16 ? 2 : 4), q, ((tokens - 1) * q_stride + row) * 2))
         return QIFT_ERR_INVALID_ARG;
-    const int64_t need = qift::attention_workspace_bytes(a);
+    const int64_t need = qift::attention_workspace_bytes(a, deal);
     if (need > 0 && (!workspace || workspace_bytes < need)) return QIFT_ERR_INVALID_ARG;
     a.q = static_cast<const __half*>(q);
     a.q_stride = q_stride;
@@ -456,7 +458,7 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
     a.f16 = out_dt == QIFT_F16;
     a.lse = lse;
     a.workspace = static_cast<float*>(workspace);
-    return from_cuda(qift::launch_attention(a, static_cast<cudaStream_t>(stream)));
+    return from_cuda(qift::launch_attention(a, deal, static_cast<cudaStream_t>(stream)));
 }
 
 qift_status qift_device_error(void* stream, int32_t* detail) {

@@ -738,8 +738,10 @@ static Deal deal_out(const AttentionArgs& a) {
 template <int D, int NR>
 static cudaError_t launch_stream(const AttentionArgs& a, const Deal& d, cudaStream_t s) {
     const size_t smem = Shape<D>::smem(NR);
-    const cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {  // what a kernel may have without asking
+        const cudaError_t e = ensure_smem(stream_kernel<D, NR>, smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)d.blocks(a.kv_heads));
     cfg.blockDim = dim3(32 * kWarps);
@@ -791,25 +793,24 @@ static thread_local int g_attention_path = kAttentionAuto;
 void debug_set_attention_path(int path) { g_attention_path = path; }
 int debug_attention_path() { return g_attention_path; }
 
-bool attention_supported(const AttentionArgs& a) {
+bool plan_attention(const AttentionArgs& a, attn::Deal* deal) {
     if (debug_attention_path() == kAttentionWide && a.head_dim > 128) return false;
     // Rows of the batch and of a launch in 32 bits, before anything is computed from their numbers.
     if ((int64_t)a.batch * a.max_q > 0x7fffffff / a.q_heads || a.tokens > 0x7fffffff / a.q_heads) return false;
-    const attn::Deal d = attn::deal_out(a);
+    const attn::Deal d = *deal = attn::deal_out(a);
     return d.of(true, a.batch).blocks(a.kv_heads) <= 0x7fffffff && d.of(false, a.batch).blocks(a.kv_heads) <= 0x7fffffff;
 }
 
-int64_t attention_workspace_bytes(const AttentionArgs& a) {
-    return a.tokens * a.q_heads * attn::deal_out(a).slots * (a.head_dim + 2) * 4;
+int64_t attention_workspace_bytes(const AttentionArgs& a, const attn::Deal& deal) {
+    return a.tokens * a.q_heads * deal.slots * (a.head_dim + 2) * 4;
 }
 
-cudaError_t launch_attention(AttentionArgs a, cudaStream_t s) {
+cudaError_t launch_attention(AttentionArgs a, const attn::Deal& deal, cudaStream_t s) {
     a.norm = a.block ? (float)(1.0 / sqrt((double)a.block)) : 1.0f;
-    const attn::Deal d = attn::deal_out(a);
     switch (a.head_dim) {
-        case 64: return attn::launch_all<64>(a, d, s);
-        case 128: return attn::launch_all<128>(a, d, s);
-        case 256: return attn::launch_all<256>(a, d, s);
+        case 64: return attn::launch_all<64>(a, deal, s);
+        case 128: return attn::launch_all<128>(a, deal, s);
+        case 256: return attn::launch_all<256>(a, deal, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -161,9 +161,40 @@ struct AttentionArgs {
     float* lse;                 // [tokens][q_heads] or null
     float* workspace;
 };
-bool attention_supported(const AttentionArgs& a);
-int64_t attention_workspace_bytes(const AttentionArgs& a);
-cudaError_t launch_attention(AttentionArgs a, cudaStream_t s);
+namespace attn {
+// How the blocks of a launch are dealt out: first the prefix's (row tile, kv head, split), then each
+// sequence's.  A split is a run of `*_chunk` steps of the kernel's key blocks.  The two kinds may go to
+// different kernels; the launch of one then has no tiles of the other kind.
+struct Deal {
+    int prefix_tiles, prefix_splits, prefix_chunk;
+    int own_tiles, own_splits, own_chunk;
+    int64_t own_sets;  // row tiles of all sequences: own_tiles of each, or as ragged_tile finds them
+    bool own_ragged;
+    // If not 0: sequences of at most `few` rows a kv head go to the streaming kernel, the others to the one for many.
+    int few, few_splits, few_chunk;
+    int slots;  // partial results a row has room for; 0: one split and no prefix, rows are finished at once
+    bool prefix_wide, own_wide;  // whether the kernel for many rows takes them
+    int64_t blocks(int kv_heads) const {
+        return (int64_t)kv_heads * ((int64_t)prefix_tiles * prefix_splits + own_sets * own_splits);
+    }
+    // What one of the two kernels has to do.
+    Deal of(bool wide, int batch) const {
+        Deal d = *this;
+        if (prefix_wide != wide) d.prefix_tiles = 0;
+        if (few && !wide) {
+            d.own_tiles = 1, d.own_splits = few_splits, d.own_chunk = few_chunk, d.own_sets = batch, d.own_ragged = false;
+        } else if (own_wide != wide) {
+            d.own_sets = 0;
+        }
+        return d;
+    }
+    __device__ __forceinline__ bool is_few(int64_t rows) const { return few && rows <= few; }
+};
+}  // namespace attn
+// How a call of these sizes is dealt out; false: the kernels cannot number its rows or blocks.
+bool plan_attention(const AttentionArgs& a, attn::Deal* deal);
+int64_t attention_workspace_bytes(const AttentionArgs& a, const attn::Deal& deal);
+cudaError_t launch_attention(AttentionArgs a, const attn::Deal& deal, cudaStream_t s);
 // Test hook: pins the attention kernel of every row set (per host thread).
 enum AttentionPath { kAttentionAuto = 0, kAttentionStream = 1, kAttentionWide = 2 };
 void debug_set_attention_path(int path);
