@@ -22,9 +22,10 @@
 // keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
 //
 // What bounds it: the bytes of the codes and scales at best (64 sequences of 8000-16384 keys, 32 query and 8
-// key/value heads of 128: 165 us, 5.1 TB/s, 78% of a copy's rate), instruction issue in fact: a step of 32 keys is
-// 465 instructions of a warp, 224 of them on the integer pipe at half rate, and 160 of all make binary16 of
-// nibbles.  So a long run of it follows the clock (186 us under the power limit).  Tried and slower: shifts as
+// key/value heads of 128: 165 us, 5.1 TB/s, 78% of a copy's rate); in fact the chain of a step, codes to scores
+// to weights to products, of which four warps a scheduler run side by side: 465 instructions for 32 keys, 224 of
+// them on the integer pipe at half rate and 160 to make binary16 of nibbles; issue is active 62%, the integer pipe
+// 54%, the tensor pipe 28%.  So a long run of it follows the clock (178-189 us under the power limit).  Tried and slower: shifts as
 // high products on the multiply pipe (186 us for 177 then), five blocks an SM with fewer registers (208),
 // three stages of copies, eight warps a block.  One query head a kv head fills one of eight columns of
 // the products at the same cost a key: 16 sequences of 300-4096 keys by 32 heads take 45 us, 3.4 TB/s.

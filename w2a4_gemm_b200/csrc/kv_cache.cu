@@ -12,7 +12,7 @@
 // lines, the half-split rotation's pairs lie in one lane, and the transform needs shuffles only between
 // its three first and its last stage.  A lane's rows are heads of one token: the position's cosines and
 // sines are read once for them.
-// What bounds it: instruction issue (3.0 of 4 a cycle): 8192 tokens of 32 query and 32 + 32 key and value heads of
+// What bounds it: instruction issue (3.1 of 4 a cycle): 8192 tokens of 32 query and 32 + 32 key and value heads of
 // 128 take 109 us, 2.8 TB/s, about 32 instructions a value, most of them the butterflies, their exchange and the
 // roundings whose order and number the format fixes; reading the rows back 31 us, 5.5 TB/s.  Few tokens: the launch,
 // 3.4 us for both.  Sums and products of two values at a time (fp32 pairs) gained nothing over the moves
