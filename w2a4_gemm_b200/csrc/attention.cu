@@ -107,9 +107,14 @@ __device__ __forceinline__ void lds(uint32_t (&r)[BYTES / 4], const uint8_t* p) 
     }
 }
 
+// Blocks an SM that the registers must leave room for.  Eight rows: four (three: 131071 keys 41 us for 36; five at
+// head_dim 64: 33 windows of 4096 keys 32.5 us for 27.3).  Sixteen rows at head_dim 64: three (32 x 8192 keys by 4
+// kv heads 42.3 us, two 49.4, four 42.0, but 16 x 3000 by 4 14.2, 18.1 and 16.2); at 128 three gain 5% on long
+// batches and lose 13% on a short prefix (15.6 us for 13.8).
+constexpr int blocks_per_sm(int D, int NR) { return D > 128 ? 1 : NR == 1 ? 4 : D == 64 ? 3 : 1; }
 // Eight query rows are the columns of one product tile; NR of them a block.
 template <int D, int NR>
-__global__ void __launch_bounds__(32 * kWarps, NR == 1 && D <= 128 ? 4 : 1) stream_kernel(const AttentionArgs a, const Deal deal) {
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kernel(const AttentionArgs a, const Deal deal) {
     using S = Shape<D>;
     constexpr int R = 8 * NR;
     extern __shared__ __align__(16) uint8_t raw[];
