@@ -280,7 +280,8 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *   out       : [tokens][q_heads][head_dim], out_dt QIFT_F16 (one rounding) or QIFT_F32; must not
  *               overlap q.
  *   lse       : fp32 [tokens][q_heads] or NULL: log of the sum of exp(scale * q.k) over visible keys.
- *               A row that sees no key has out 0 and lse -infinity; one whose q holds a NaN has NaN in both.
+ *               A row that sees no key has out 0 and lse -infinity, whatever its q holds; one that sees any
+ *               and whose q holds a NaN or an infinity has NaN in both.
  *   workspace : device memory of at least qift_paged_attention_workspace() bytes (16-byte aligned),
  *               NULL where that is 0.  Two calls that may run at once, or captured graphs that may,
  *               need one each.

@@ -776,3 +776,43 @@ def test_tokens_whose_elements_pass_32_bits():
     s_max = small[1].nan_to_num(0.0).amax()
     e_u = score_error(q[-last:].double().abs().sum(-1) * s_max / math.sqrt(d), d)
     assert ((lse[-last:].double() - u).abs() <= reach * 2.0 ** -11 + e_u + 2.0 ** -16 + u.abs() * 2.0 ** -20).all()
+
+
+# ------------------------------------------------------------------------------------------ numbers at their ends
+@pytest.mark.parametrize("prefix", [0, 16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_an_infinite_query_gives_no_number_whatever_the_codes_signs(d, prefix):
+    """Every key a row sees may answer an infinity with -infinity (or with infinity, or by a code of 0 with NaN): no
+    softmax is defined, and the row must not be taken for one that sees nothing."""
+    hq, hk, size, n = 4, 2, 16, 9
+    m = make([n], [prefix + n], hq, hk, d, size, prefix, seed=30 + d)
+    ref, lse, A, reach = reference(m)
+    for sign in (7, -7, 0):
+        for at in (0, 1, 2, 5, 8, d // 2, d - 2, d - 1):
+            cache = [c.clone() for c in m["cache"]]
+            if at % 2:
+                cache[0][..., at // 2] = (cache[0][..., at // 2] & 0x0F) | ((sign & 15) << 4)
+            else:
+                cache[0][..., at // 2] = (cache[0][..., at // 2] & 0xF0) | (sign & 15)
+            x = dict(m, cache=cache, q=m["q"].clone())
+            ref, lse, A, reach = reference(x)
+            bad = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+            bad[0, 1] = bad[0, 2] = bad[n - 1, 3] = True   # position prefix sees one key of its own
+            x["q"][0, 1, at], x["q"][0, 2, at], x["q"][n - 1, 3, at] = math.inf, -math.inf, math.inf
+            for path in paths(m):
+                qg.qift_debug_set_attention_path(path)
+                l = torch.empty(n, hq, device="cuda")
+                out = call(x, out_dtype=torch.float32, lse=l)
+                assert torch.isnan(out[bad]).all() and torch.isnan(l[bad]).all(), (path, sign, at, l[bad].tolist())
+                assert ((out.double() - ref).abs() <= bound(A, reach, ref, False))[~bad].all(), (path, sign, at)
+                assert torch.isfinite(l[~bad]).all()
+
+
+def test_an_infinite_query_that_sees_nothing_is_empty():
+    m = make([5], [3], 4, 2, 64, 16, seed=31)               # the first two rows stand before the sequence
+    m["q"][0, 1, 4], m["q"][1, 2, 7] = math.inf, NAN
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        l = torch.zeros(5, 4, device="cuda")
+        out = call(m, out_dtype=torch.float32, lse=l)
+        assert (out[:2] == 0).all() and (l[:2] == -math.inf).all() and torch.isfinite(out[2:]).all()

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
         for (int w = 0; w < S::KW; ++w) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             const int d = (w / 4) * 128 + (D >= 128 ? 32 : 16) * t + 8 * (w % 4);
-            if (token >= 0) x = *reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (int64_t)head * D + d);
+            if (token >= 0) x = no_infinity(*reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (int64_t)head * D + d));
             qf[n][w][0] = prmt(x.x, x.z, 0x5410u);  // values 0, 4 of the eight that meet a word's nibbles
             qf[n][w][1] = prmt(x.x, x.z, 0x7632u);  // 1, 5
             qf[n][w][2] = prmt(x.y, x.w, 0x5410u);  // 2, 6

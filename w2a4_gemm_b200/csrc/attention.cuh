@@ -11,7 +11,7 @@
 // Partial results of a row over a set S of keys, with u_j = scale log2(e) q.k_j:
 //   M, L = sum_S 2^(u_j - M), O = sum_S 2^(u_j - M) v_j
 // and any number of them join by M* = max M, L* = sum L 2^(M - M*), O* likewise.  An empty set has
-// M = kNone, L = 0, and no O; a row with a NaN or infinity in q has L = NaN, which stays one.
+// M = kNone, L = 0, and no O; a row with a NaN or infinity in q has L = NaN over any other, which stays one.
 #pragma once
 
 #include "common.cuh"
@@ -150,6 +150,17 @@ constexpr int kWideStep = 128;  // keys it takes at a time
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two query values with an infinity made NaN (x 0 + x; any other value stays what it is).  An infinity times the
+// codes of the keys a row sees may be -infinity for all of them, and the row would look like one that sees nothing;
+// its softmax is not defined, so its scores are NaN, whatever the codes (also 0) are.
+__device__ __forceinline__ uint32_t no_infinity(uint32_t x) {
+    const __half2 v = *reinterpret_cast<const __half2*>(&x);
+    const __half2 r = __hfma2(v, __float2half2_rn(0.0f), v);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint4 no_infinity(uint4 x) {
+    return make_uint4(no_infinity(x.x), no_infinity(x.y), no_infinity(x.z), no_infinity(x.w));
 }
 // Two two's-complement nibbles, 16 bits apart, as binary16: from bits 0-3 exactly, from bits 4-7
 // plus 72 (1 x 2^6 with the nibble, its sign bit flipped, above the last four bits), or exactly.

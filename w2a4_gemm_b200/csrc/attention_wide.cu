@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 32 / PER; ++q) {
                 const int k = q * PER + lane / PIECES;
+                x[q] = no_infinity(x[q]);
                 sts128(dst + k * 128 + (((c & 7) ^ (k & 7)) << 4), prmt(x[q].x, x[q].z, 0x5410u),
                        prmt(x[q].x, x[q].z, 0x7632u), prmt(x[q].y, x[q].w, 0x5410u), prmt(x[q].y, x[q].w, 0x7632u));
             }
