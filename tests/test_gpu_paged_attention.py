@@ -816,3 +816,40 @@ def test_an_infinite_query_that_sees_nothing_is_empty():
         l = torch.zeros(5, 4, device="cuda")
         out = call(m, out_dtype=torch.float32, lse=l)
         assert (out[:2] == 0).all() and (l[:2] == -math.inf).all() and torch.isfinite(out[2:]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("behind", [None, 0.0, 300.0])
+@pytest.mark.parametrize("n", [190, 3000])
+def test_keys_with_zero_values_far_above_the_others(n, behind, d):
+    """Keys whose value rows are all zero (a scale of 0) meet no product that could overflow, but their weights are
+    in the sum: scores up to 2^140 above those before, one sequence for each, with a last key further above or not.
+
+    A weight is held to 2^-29 of the largest weight times its value's scale, a scale below 2^-28 counting as 2^-28:
+    7 codes times n such errors of weights up to 1 are added to the bound."""
+    B, hq = 75, 4
+    m = make([1] * B, [n] * B, hq, 1, d, 16, seed=n + d)
+    kc, ks, vc, vs = m["cache"]
+    kc.zero_()
+    kc[..., 0] = 7                                          # a key is (7, 0, 0, ...) s, a query (1, 0, 0, ...)
+    m["q"].zero_()
+    m["q"][..., 0] = 1
+    for b in range(B):
+        at = torch.arange(n, device="cuda")
+        page, row = m["table"][b].long()[at // 16], at % 16
+        log2 = torch.zeros(n, device="cuda")
+        log2[n // 2:] = 103 + 0.5 * b
+        if behind is not None:
+            log2[-1] = behind
+        ks[page, 0, row] = log2 * math.log(2) * math.sqrt(d) / 7
+        zero = (log2 > 1) & (log2 < 299)
+        vs[page[zero], 0, row[zero]] = 0.0
+        vc[page[zero], 0, row[zero]] = 0
+    ref, lse, A, reach = reference(m)
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        l = torch.empty(B, hq, device="cuda")
+        out = call(m, out_dtype=torch.float32, lse=l)
+        e_u = score_error(reach, d) + 2.0 ** -16 + lse.abs() * 2.0 ** -20
+        assert ((l.double() - lse).abs() <= e_u).all(), (path, (l - lse).abs().amax(1).tolist())
+        assert ((out.double() - ref).abs() <= bound(A, reach, ref, False) + 7 * n * 2.0 ** -57).all(), path

@@ -371,25 +371,28 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
         }
 
         // ---- weights, by the reference so far.  It is raised, and what is summed scaled down, only where a
-        // weight would pass kMostWeight (or is no number: an overflow times a scale of 0); a vote
-        // decides, so all lanes of a row agree.
-        float wt[2][NR][4];
+        // weight would pass kMostWeight, or this lane's sum kMostSum (or one is no number: an overflow times a
+        // scale of 0); a vote decides, so all lanes of a row agree.
+        float part[NR][2];
         __half2 wv[2][NR][2];
         const __half2 most = __float2half2_rn(kMostWeight);
         auto weigh = [&]() {
             bool fits = true;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int n = 0; n < NR; ++n) {
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            wt[c][n][2 * e + q] = ex2(__fmaf_rn(x[c][n][2 * e + q], ks[c][e], -refl[n][q]));
-                        wv[c][n][e] = __floats2half2_rn(wt[c][n][2 * e] * vs[c][e], wt[c][n][2 * e + 1] * vs[c][e]);
+                        const float w0 = ex2(__fmaf_rn(x[c][n][2 * e], ks[c][e], -refl[n][0]));
+                        const float w1 = ex2(__fmaf_rn(x[c][n][2 * e + 1], ks[c][e], -refl[n][1]));
+                        wv[c][n][e] = __floats2half2_rn(w0 * vs[c][e], w1 * vs[c][e]);
                         fits = fits && __hble2(wv[c][n][e], most);
+                        part[n][0] = c + e ? part[n][0] + w0 : w0;
+                        part[n][1] = c + e ? part[n][1] + w1 : w1;
                     }
+                fits = fits && part[n][0] <= kMostSum && part[n][1] <= kMostSum;
+            }
             return fits;
         };
         if (!__all_sync(0xffffffffu, weigh())) {
@@ -401,8 +404,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)  // the smallest scale is 2^-24 / 7
-                            top = fmaxf(top, __fmaf_rn(x[c][n][2 * e + q], ks[c][e], fmaxf(lg2(vs[c][e]), -28.0f)));
+                        for (int e = 0; e < 2; ++e)
+                            top = fmaxf(top, __fmaf_rn(x[c][n][2 * e + q], ks[c][e], fmaxf(lg2(vs[c][e]), kLeastScale)));
 #pragma unroll
                     for (int m = 4; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
                     const float down = ex2(refl[n][q] + kLift - top);
@@ -416,16 +419,14 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
 
         // ---- the second product
 #pragma unroll
+        for (int n = 0; n < NR; ++n) sum[n][0] += part[n][0], sum[n][1] += part[n][1];
+#pragma unroll
         for (int c = 0; c < 2; ++c) {
             uint32_t p[NR][2];
 #pragma unroll
             for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sum[n][0] += wt[c][n][2 * e];
-                    sum[n][1] += wt[c][n][2 * e + 1];
-                    p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&wv[c][n][e]));
-                }
+                for (int e = 0; e < 2; ++e) p[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&wv[c][n][e]));
             // Four codes of a key are a 16-bit unit; the transposing load of 8 keys by 8 units leaves unit g of
             // keys 2t and 2t + 1 in a lane's register, as the left operand wants its pairs.  Four such loads an
             // instruction: units 8 u + g of keys 0-7 and 8-15, for two u.

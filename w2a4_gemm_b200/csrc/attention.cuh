@@ -30,6 +30,12 @@ __device__ __forceinline__ uint8_t* aligned(uint8_t* raw) {
 }
 
 constexpr float kNone = -1e30f;  // finite, so that the difference of two of them is a number
+// A key whose values are all zero (value scale 0) adds nothing to O, so only the sum bounds its weight: a step's
+// weights of a row may sum to this much before the row's reference is raised.  A value scale below 2^kLeastScale
+// counts as that much where it is (the smallest a row of binary16 values can have is 2^-24 / 7).  So weights stay below
+// 2^48 without another raise, and the sum of 2^30 of them below 2^78: no sum, nor the join of any, overflows.
+constexpr float kMostSum = 281474976710656.0f;  // 2^48
+constexpr float kLeastScale = -28.0f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

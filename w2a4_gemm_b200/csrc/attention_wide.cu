@@ -22,7 +22,8 @@
 // One tile's products run under the other's softmax.
 //
 // A row's reference is raised (and O scaled down) only when the weights of a half step might not fit
-// binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j.
+// binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j, or times
+// kMostWeight / kMostSum where that is more, so that the sum itself stays below kMostSum.
 //
 // What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 581 us, 59% of the
 // measured bf16 matrix rate over the visible half, 614 us in a long run under the power limit): a step of 256
@@ -284,7 +285,7 @@ __device__ __forceinline__ float largest(uint32_t taddr, const float* ks, const 
         const uint32_t seen = mask ? view.bits(first + c * 32) : 0xFFFFFFFFu;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            const float u = __fmaf_rn(__uint_as_float(x[i]), ks[c * 32 + i], fmaxf(lg2(ts[c * 32 + i]), -28.0f));
+            const float u = __fmaf_rn(__uint_as_float(x[i]), ks[c * 32 + i], fmaxf(lg2(ts[c * 32 + i]), kLeastScale));
             if (seen & (1u << i)) top = fmaxf(top, u);
         }
     }
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float t = good ? vs : 0.0f;
             key_scales[ring * BN + u] = good ? ks * a.scale_log2 : __int_as_float(0x7fffffff);
             value_scales[ring * BN + u] = t;
-            float top = t;  // of this warp's 32 keys
+            float top = fmaxf(t, kMostWeight / kMostSum);  // of this warp's 32 keys, for the test of their sum
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
             if (lane == 0) reinterpret_cast<float*>(most + ring)[w] = top;
