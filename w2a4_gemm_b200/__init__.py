@@ -6,9 +6,11 @@ Inference" (Huang, Tsai), Abstract: Hadamard-rotated weights and activations, fi
 
 The functions here carry the C ABI's names (``include/qift.h``) and only marshal arguments:
 they check devices, dtypes and shapes, allocate outputs with torch, and pass raw device
-pointers plus the current CUDA stream to the library.  Every step of the path runs in the
-library's kernels.  There is no CPU fallback: without the built library or a CUDA device
-these functions raise.
+pointers plus the current CUDA stream, or the one given as ``stream``, to the library.  With
+``stream`` given, the caller orders that stream after what the call's inputs come from, and
+its own use of the results after that stream, as with any work on two streams; the results
+come from that stream's memory.  Every step of the path runs in the library's kernels.  There
+is no CPU fallback: without the built library or a CUDA device these functions raise.
 """
 from __future__ import annotations
 
@@ -104,6 +106,21 @@ def _stream(stream, device=None):
     return C.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, make, *args, **kw):
+    """What make(...) allocates for a call on `stream` to write.  With a stream given, the memory is that stream's: memory
+    of the current one may still be read by work queued there, which the call would not wait for.  The current stream,
+    where the caller goes on (ordered after `stream` by the caller), is recorded, so that a result dropped there is not
+    reused before what is queued there by then is done."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    current = torch.cuda.current_stream(t.device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _ptr(t):
     return C.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -173,7 +190,7 @@ def qift_rotate(x: torch.Tensor, block: int, out: torch.Tensor | None = None, st
     if out is not None:
         _shape(_cuda(out, "out", x.dtype), "out", x.shape)
     dev = _same_device(("x", x), ("out", out))
-    y = torch.empty_like(x) if out is None else out
+    y = _made(stream, torch.empty_like, x) if out is None else out
     n = x.shape[-1]
     rows = x.numel() // n if n else 0
     dt = QIFT_F32 if x.dtype == torch.float32 else QIFT_F16
@@ -192,9 +209,9 @@ def qift_quantize_weights(w_rot: torch.Tensor, levelset="qift", grid_points: int
     _2d(_cuda(w_rot, "w_rot", torch.float32), "w_rot")
     n_out, n_in = w_rot.shape
     dev = w_rot.device
-    codes = torch.empty((n_out, n_in // _codes_per_word(levelset)), dtype=torch.int32, device=dev)
-    scales = torch.empty(n_out, dtype=torch.float32, device=dev)
-    mse = torch.empty(n_out, dtype=torch.float64, device=dev) if with_mse else None
+    codes = _made(stream, torch.empty, (n_out, n_in // _codes_per_word(levelset)), dtype=torch.int32, device=dev)
+    scales = _made(stream, torch.empty, n_out, dtype=torch.float32, device=dev)
+    mse = _made(stream, torch.empty, n_out, dtype=torch.float64, device=dev) if with_mse else None
     with torch.cuda.device(dev):
         _check(lib().qift_quantize_weights(_ptr(w_rot), n_out, n_in, _set(levelset), grid_points, lo, hi,
                                            _ptr(codes), _ptr(scales), _ptr(mse), _stream(stream, dev)),
@@ -212,10 +229,10 @@ def qift_quantize_weights_asym(w_rot: torch.Tensor, grid_points: int = 100, lo: 
     _2d(_cuda(w_rot, "w_rot", torch.float32), "w_rot")
     n_out, n_in = w_rot.shape
     dev = w_rot.device
-    codes = torch.empty((n_out, n_in // 16), dtype=torch.int32, device=dev)
-    scales = torch.empty(n_out, dtype=torch.float32, device=dev)
-    zeros = torch.empty(n_out, dtype=torch.int32, device=dev)
-    mse = torch.empty(n_out, dtype=torch.float64, device=dev) if with_mse else None
+    codes = _made(stream, torch.empty, (n_out, n_in // 16), dtype=torch.int32, device=dev)
+    scales = _made(stream, torch.empty, n_out, dtype=torch.float32, device=dev)
+    zeros = _made(stream, torch.empty, n_out, dtype=torch.int32, device=dev)
+    mse = _made(stream, torch.empty, n_out, dtype=torch.float64, device=dev) if with_mse else None
     with torch.cuda.device(dev):
         _check(lib().qift_quantize_weights_asym(_ptr(w_rot), n_out, n_in, grid_points, lo, hi, _ptr(codes),
                                                 _ptr(scales), _ptr(zeros), _ptr(mse), _stream(stream, dev)),
@@ -230,9 +247,9 @@ def qift_rotate_quantize_weights(w: torch.Tensor, block: int, levelset="qift", g
     _2d(_cuda(w, "w", torch.float32), "w")
     n_out, n_in = w.shape
     dev = w.device
-    codes = torch.empty((n_out, n_in // _codes_per_word(levelset)), dtype=torch.int32, device=dev)
-    scales = torch.empty(n_out, dtype=torch.float32, device=dev)
-    mse = torch.empty(n_out, dtype=torch.float64, device=dev) if with_mse else None
+    codes = _made(stream, torch.empty, (n_out, n_in // _codes_per_word(levelset)), dtype=torch.int32, device=dev)
+    scales = _made(stream, torch.empty, n_out, dtype=torch.float32, device=dev)
+    mse = _made(stream, torch.empty, n_out, dtype=torch.float64, device=dev) if with_mse else None
     with torch.cuda.device(dev):
         _check(lib().qift_rotate_quantize_weights(_ptr(w), n_out, n_in, block, _set(levelset), grid_points, lo,
                                                   hi, _ptr(codes), _ptr(scales), _ptr(mse), _stream(stream, dev)),
@@ -250,8 +267,8 @@ def qift_quantize_acts(x: torch.Tensor, block: int = 0, out_q: torch.Tensor | No
     if out_scales is not None:
         _at_least(_cuda(out_scales, "out_scales", torch.float32), "out_scales", T)
     dev = _same_device(("x", x), ("out_q", out_q), ("out_scales", out_scales))
-    q = torch.empty((T, K), dtype=torch.int8, device=dev) if out_q is None else out_q
-    s = torch.empty(T, dtype=torch.float32, device=dev) if out_scales is None else out_scales
+    q = _made(stream, torch.empty, (T, K), dtype=torch.int8, device=dev) if out_q is None else out_q
+    s = _made(stream, torch.empty, T, dtype=torch.float32, device=dev) if out_scales is None else out_scales
     with torch.cuda.device(dev):
         _check(lib().qift_quantize_acts(_ptr(x), T, K, block, _ptr(q), _ptr(s), _stream(stream, dev)),
                "qift_quantize_acts")
@@ -264,8 +281,8 @@ def qift_quantize_kv(x: torch.Tensor, block: int, stream=None):
     _2d(_cuda(x, "x", torch.float16), "x")
     T, n = x.shape
     dev = x.device
-    packed = torch.empty((T, n // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(T, dtype=torch.float32, device=dev)
+    packed = _made(stream, torch.empty, (T, n // 2), dtype=torch.uint8, device=dev)
+    scales = _made(stream, torch.empty, T, dtype=torch.float32, device=dev)
     with torch.cuda.device(dev):
         _check(lib().qift_quantize_kv(_ptr(x), T, n, block, _ptr(packed), _ptr(scales), _stream(stream, dev)),
                "qift_quantize_kv")
@@ -279,7 +296,7 @@ def qift_dequantize_kv(packed: torch.Tensor, scales: torch.Tensor, block: int, s
     T, n2 = packed.shape
     _at_least(scales, "scales", T)
     dev = _same_device(("packed", packed), ("scales", scales))
-    out = torch.empty((T, 2 * n2), dtype=torch.float16, device=dev)
+    out = _made(stream, torch.empty, (T, 2 * n2), dtype=torch.float16, device=dev)
     with torch.cuda.device(dev):
         _check(lib().qift_dequantize_kv(_ptr(packed), _ptr(scales), T, 2 * n2, block, _ptr(out),
                                         _stream(stream, dev)), "qift_dequantize_kv")
@@ -310,7 +327,7 @@ def qift_linear(q: torch.Tensor, act_scale: torch.Tensor, codes: torch.Tensor, w
     if out is not None:
         _shape(_cuda(out, "out", out_dtype), "out", (T, N))
     dev = _same_device(("q", q), ("act_scale", act_scale), ("codes", codes), ("w_scale", w_scale), ("out", out))
-    y = torch.empty((T, N), dtype=out_dtype, device=dev) if out is None else out
+    y = _made(stream, torch.empty, (T, N), dtype=out_dtype, device=dev) if out is None else out
     dt = QIFT_F16 if out_dtype == torch.float16 else QIFT_F32
     with torch.cuda.device(dev):
         _check(lib().qift_linear(_ptr(q), _ptr(act_scale), _ptr(codes), _ptr(w_scale), _set(levelset), T, N, K,
@@ -345,7 +362,7 @@ def qift_decode_linear(x: torch.Tensor, block: int, codes: torch.Tensor, w_scale
         _at_least(_cuda(act_scale_out, "act_scale_out", torch.float32), "act_scale_out", T)
     dev = _same_device(("x", x), ("codes", codes), ("w_scale", w_scale), ("out", out), ("q_out", q_out),
                        ("act_scale_out", act_scale_out))
-    y = torch.empty((T, N), dtype=out_dtype, device=dev) if out is None else out
+    y = _made(stream, torch.empty, (T, N), dtype=out_dtype, device=dev) if out is None else out
     dt = QIFT_F16 if out_dtype == torch.float16 else QIFT_F32
     with torch.cuda.device(dev):
         _check(lib().qift_decode_linear(_ptr(x), T, K, block, _ptr(codes), _ptr(w_scale), _set(levelset), N, _ptr(y),
@@ -473,7 +490,10 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
         if hq == 0:
             raise ValueError("q must have at least one head")
         if q_out is None:
-            q_out = torch.empty_like(q) if T <= 1 or q_row == hq * d else q.new_empty((T, hq, d))
+            if stream is not None:
+                q_out = _made(stream, q.new_empty, (T, hq, d))
+            else:
+                q_out = torch.empty_like(q) if T <= 1 or q_row == hq * d else q.new_empty((T, hq, d))
             out_at = q_out.data_ptr()
         else:
             out_at = _is(q_out, "q_out", _F16, (T, hq, d), index)
@@ -497,8 +517,11 @@ def qift_gather_kv(k_cache: torch.Tensor, k_scales: torch.Tensor, v_cache: torch
     kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)
     T = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() else 0
     slots_at = _is(slots, "slots", _I64, (T,), index)
-    k = k_scales.new_empty((T, kv_heads, d), dtype=_F16)
-    v = torch.empty_like(k)
+    if stream is None:
+        k = k_scales.new_empty((T, kv_heads, d), dtype=_F16)
+        v = torch.empty_like(k)
+    else:
+        k, v = (_made(stream, k_scales.new_empty, (T, kv_heads, d), dtype=_F16) for _ in range(2))
     status = _launch(index, (_lib or lib()).qift_gather_kv, (
         kc, ks, vc, vs, pages, size, kv_heads, d, slots_at, T, block, k.data_ptr(), v.data_ptr(), _on(stream, index)))
     if status:
@@ -564,8 +587,11 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
                 workspace = k_cache.new_empty(need)
         ws_at, ws_bytes = workspace.data_ptr(), need
     if out is None:
-        plain = out_dtype is _F16 and (T <= 1 or q_row == hq * d)
-        out = torch.empty_like(q) if plain else q.new_empty(shape, dtype=out_dtype)
+        if stream is not None:
+            out = _made(stream, q.new_empty, shape, dtype=out_dtype)
+        else:
+            plain = out_dtype is _F16 and (T <= 1 or q_row == hq * d)
+            out = torch.empty_like(q) if plain else q.new_empty(shape, dtype=out_dtype)
         out_at = out.data_ptr()
     else:
         out_at = _is(out, "out", out_dtype, shape, index)
