@@ -853,3 +853,15 @@ def test_keys_with_zero_values_far_above_the_others(n, behind, d):
         e_u = score_error(reach, d) + 2.0 ** -16 + lse.abs() * 2.0 ** -20
         assert ((l.double() - lse).abs() <= e_u).all(), (path, (l - lse).abs().amax(1).tolist())
         assert ((out.double() - ref).abs() <= bound(A, reach, ref, False) + 7 * n * 2.0 ** -57).all(), path
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (8, 0), (0, 0)])
+def test_an_empty_rope_table_is_refused_and_not_taken_for_none(shape):
+    cache = empty_cache(1, 1, 16, 64)
+    x = torch.randn(2, 1, 64, device="cuda", generator=gen(1)).half()
+    at = torch.arange(2, device="cuda")
+    q_out = torch.full((2, 1, 64), 5.0, device="cuda").half()
+    with pytest.raises(ValueError, match="rope"):
+        qg.qift_append_kv(x, x, at, 64, *cache, q=x, positions=at, rope=torch.empty(shape, device="cuda"), q_out=q_out)
+    torch.cuda.synchronize()
+    assert (q_out == 5).all() and torch.isnan(cache[1]).all() and torch.isnan(cache[3]).all()

@@ -483,6 +483,8 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
             _2d(_cuda(rope, "rope", _F32), "rope")
         rope_len, rope_dim = shape = rope.shape
         rope_at = _is(rope, "rope", _F32, shape, index)
+        if not (rope_len and rope_dim):  # without an address it would pass for no rotation at all
+            raise ValueError(f"rope must hold at least one position and one pair, got shape {tuple(shape)}")
         positions_at = _is(positions, "positions", _I64, (T,), index)
     if q is not None:
         hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
