@@ -865,3 +865,64 @@ def test_an_empty_rope_table_is_refused_and_not_taken_for_none(shape):
         qg.qift_append_kv(x, x, at, 64, *cache, q=x, positions=at, rope=torch.empty(shape, device="cuda"), q_out=q_out)
     torch.cuda.synchronize()
     assert (q_out == 5).all() and torch.isnan(cache[1]).all() and torch.isnan(cache[3]).all()
+
+
+def guarded(shape, dtype, fill=77):
+    """A tensor inside a larger one, and what tells whether anything around it was written."""
+    n = math.prod(shape)
+    whole = torch.full((n + 2 * 4096,), fill, dtype=dtype, device="cuda")
+    return whole[4096:4096 + n].view(shape), lambda: bool((whole[:4096] == fill).all() and (whole[4096 + n:] == fill).all())
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (16, 1, 128), (3, 3, 256)])
+def test_contradicting_offsets_write_nowhere_else(hq, hk, d, prefix):
+    """Offsets, lengths and tables that contradict the call's sizes: nothing around the result, its log-sum-exp and the
+    workspace is written, and under bounds checks no index leaves its array."""
+    q_lens, size = [1, 2, 0, 30, 1, 1, 5, 1], 16
+    m = make(q_lens, [prefix + 40 + 90 * (i % 4) for i in range(8)], hq, hk, d, size, prefix, seed=33)
+    T, far = sum(q_lens), 2 ** 31 - 1
+    starts = [m["cu_q"].tolist(), [0, 3, 2, 1, 9, 9, 4, 40, 2], [-5, 2, 4, -far, 0, 7, 11, 12, 400], [far] * 9, [-far] * 9,
+              [0] * 8 + [T], [0] * 8 + [far], [T] + [0] * 8, [T - 1] * 9, list(range(T, T - 9, -1)), [0, T, 0, T, 0, T, 0, T, 0]]
+    lens = [m["kv_lens"].tolist(), [far, -far, -3, 0, 2 ** 30, far, 1, -1]]
+    tables = [m["table"], torch.full_like(m["table"], far), torch.full_like(m["table"], -far)]
+    for path in paths(m):
+        qg.qift_debug_set_attention_path(path)
+        for max_q in (1, 7, 30):
+            for max_kv in (0, 1):
+                bytes_ = qg.qift_paged_attention_workspace(T, hq, hk, d, 8, max_q, size, m["table"].shape[1], max_kv, prefix)
+                for cu in starts:
+                    for n in lens:
+                        for table in tables:
+                            out, out_ok = guarded((T, hq, d), torch.float16)
+                            l, l_ok = guarded((T, hq), torch.float32)
+                            ws, ws_ok = guarded((bytes_,), torch.uint8)
+                            call(dict(m, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_q=max_q, table=table,
+                                      kv_lens=torch.tensor(n, dtype=torch.int32, device="cuda")),
+                                 out=out, lse=l, workspace=ws, max_kv=max_kv, block=d)
+                            assert out_ok() and l_ok() and ws_ok(), (path, max_q, max_kv, cu, n)
+
+
+@pytest.mark.parametrize("d,rope_dim,interleaved", [(64, 64, False), (128, 48, True), (256, 128, False)])
+def test_append_and_gather_write_nowhere_else(d, rope_dim, interleaved):
+    T, hq, hk, size, pages, far = 21, 5, 3, 16, 3, 50
+    g = gen(34)
+    x = torch.randn(T, hq + 2 * hk, d, device="cuda", generator=g).half()
+    edge = [-1, -2 ** 63, 2 ** 63 - 1, pages * size, pages * size - 1, 0, 2 ** 31, -2 ** 31, 2 ** 32]
+    slots = torch.tensor(edge + list(range(1, T - len(edge) + 1)), device="cuda")
+    positions = torch.tensor(list(range(12)) + [far - 1, far, -1, 2 ** 62, -2 ** 63, 2 ** 63 - 1, 2 ** 32, 0, 0], device="cuda")
+    made = [guarded((pages, hk, size, d // 2), torch.uint8), guarded((pages, hk, size), torch.float32),
+            guarded((pages, hk, size, d // 2), torch.uint8), guarded((pages, hk, size), torch.float32),
+            guarded((T, hq, d), torch.float16)]
+    cache = [t for t, _ in made[:4]]
+    qg.qift_append_kv(x[:, hq:hq + hk], x[:, hq + hk:], slots, d, *cache, q=x[:, :hq], positions=positions,
+                      rope=rope_table(far, rope_dim).cuda(), interleaved=interleaved, q_out=made[4][0])
+    assert all(ok() for _, ok in made)
+    kept = ((slots >= 0) & (slots < pages * size) & (positions >= 0) & (positions < far)).tolist()
+    written = {int(s) for s, k in zip(slots.tolist(), kept) if k}
+    for s in cache[1::2]:
+        now = (s.movedim(1, 2).reshape(pages * size, hk) != 77).all(1)
+        assert {i for i, w in enumerate(now.tolist()) if w} == written
+    k, v = qg.qift_gather_kv(*cache, slots, d)
+    outside = (slots < 0) | (slots >= pages * size)
+    assert (k[outside] == 0).all() and (v[outside] == 0).all()

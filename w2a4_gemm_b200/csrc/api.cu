@@ -458,6 +458,7 @@ qift_status qift_paged_attention(const void* q, int64_t q_stride, int64_t tokens
     a.f16 = out_dt == QIFT_F16;
     a.lse = lse;
     a.workspace = static_cast<float*>(workspace);
+    a.workspace_bytes = workspace_bytes;
     return from_cuda(qift::launch_attention(a, deal, static_cast<cudaStream_t>(stream)));
 }
 

@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
         for (int w = 0; w < S::KW; ++w) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             const int d = (w / 4) * 128 + (D >= 128 ? 32 : 16) * t + 8 * (w % 4);
-            if (token >= 0) x = no_infinity(*reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (int64_t)head * D + d));
+            const int64_t at = token * a.q_stride + (int64_t)head * D + d;
+            if (token >= 0 && in_queries(a, at, 8)) x = no_infinity(*reinterpret_cast<const uint4*>(a.q + at));
             qf[n][w][0] = prmt(x.x, x.z, 0x5410u);  // values 0, 4 of the eight that meet a word's nibbles
             qf[n][w][1] = prmt(x.x, x.z, 0x7632u);  // 1, 5
             qf[n][w][2] = prmt(x.y, x.w, 0x5410u);  // 2, 6
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
         const int s = s_begin + warp + (turn + (lane >> 1)) * kWarps;
         const int j = (s + (s >= range.head ? shift : 0)) * kStep + (lane & 1) * 16;
         places = kNowhere;
-        if (s < s_end && j < range.limit) {
+        if (s < s_end && j < range.limit && in_table(a, prefix, j >> a.log_page)) {
             const int page = table[j >> a.log_page];
             if ((uint32_t)page < (uint64_t)a.n_pages)
                 places = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & page_mask)) >> 4);
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(D, NR)) stream_kern
         } else {
             const Parts p = parts(a, deal.slots);
             const int64_t at = (token * a.q_heads + head) * deal.slots + (prefix ? split : deal.prefix_splits + split);
+            if (!in_parts(a, deal.slots, at)) continue;
             if (lane == 0) p.ml[at] = make_float2(M, L);
             if (!(L == 0.0f)) {
 #pragma unroll
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
     if (token < 0) return;
     const Parts p = parts(a, deal.slots);
     const int64_t at = (token * a.q_heads + head) * deal.slots;
-    const float2 ml = lane < slots ? p.ml[at + lane] : make_float2(kNone, 0.0f);
+    const float2 ml = lane < slots && in_parts(a, deal.slots, at + lane) ? p.ml[at + lane] : make_float2(kNone, 0.0f);
     float M = ml.x;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const AttentionArgs a, co
             w[u] = __shfl_sync(0xffffffffu, f, (k0 + u) & 31);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
-            if (k0 + u < slots && !(w[u] == 0.0f)) {  // an empty slot's O was never written
+            if (k0 + u < slots && !(w[u] == 0.0f) && in_parts(a, deal.slots, at + k0 + u)) {  // an empty slot's O was never written
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     *reinterpret_cast<float2*>(&v[u][e]) =
@@ -586,7 +588,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     const Parts p = parts(a, deal.slots);
     const int64_t at = (token * a.q_heads + head) * deal.slots;
     float M = kNone;
-    for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) M = fmaxf(M, p.ml[at + k].x);
+    for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps)
+        if (in_parts(a, deal.slots, at + k)) M = fmaxf(M, p.ml[at + k].x);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
     if (lane == 0) red[0][warp] = M;
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
     for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[0][w]);
     float L = 0.0f, acc[E];
     for (int k = threadIdx.x; k < slots; k += 32 * kJoinWarps) {
-        const float2 ml = p.ml[at + k];
+        const float2 ml = in_parts(a, deal.slots, at + k) ? p.ml[at + k] : make_float2(kNone, 0.0f);
         const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
         weight[k] = f;
         L += f * ml.y;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const AttentionAr
             w[u] = k < slots ? weight[k] : 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) v[u][e] = 0.0f;
-            if (!(w[u] == 0.0f)) {  // an empty slot's O was never written
+            if (!(w[u] == 0.0f) && in_parts(a, deal.slots, at + k)) {  // an empty slot's O was never written
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     *reinterpret_cast<float2*>(&v[u][e]) = *reinterpret_cast<const float2*>(p.o + (at + k) * D + lane * E + e);

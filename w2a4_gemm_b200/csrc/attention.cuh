@@ -55,7 +55,8 @@ struct Sequence {
     int q_len, kv_len;
 };
 __device__ __forceinline__ Sequence sequence(const AttentionArgs& a, int b) {
-    Sequence s;
+    Sequence s = {0, 0, 0};
+    if (!QIFT_CK_RANGE(b, 1, a.batch)) return s;
     if (a.cu_q) {
         int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
         lo = lo < 0 ? 0 : lo;
@@ -78,7 +79,7 @@ __device__ __forceinline__ int sequence_of(const AttentionArgs& a, int64_t token
     int lo = 0, hi = a.batch;  // first b in [lo, hi] with cu_q[b] > token
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] > token) hi = mid;
+        if (QIFT_CK_RANGE(mid, 1, a.batch) && a.cu_q[mid] > token) hi = mid;
         else lo = mid + 1;
     }
     const int b = lo - 1;
@@ -133,7 +134,7 @@ __device__ __forceinline__ Range visible(const AttentionArgs& a, int pmin, int p
 template <int PER>
 __device__ __forceinline__ bool ragged_tile(const AttentionArgs& a, int64_t x, uint32_t G, int& b, int& tile) {
     auto start = [&](int s) {
-        int64_t first = a.cu_q[s];
+        int64_t first = QIFT_CK_RANGE(s, 1, a.batch) ? a.cu_q[s] : 0;
         first = first < 0 ? 0 : first > a.tokens ? a.tokens : first;
         return first * G / PER + s;
     };
@@ -204,6 +205,23 @@ __host__ __device__ inline Parts parts(const AttentionArgs& a, int slots) {
     return p;
 }
 
+// Bounds-checked build: query values, result rows and partial results lie inside the caller's arrays.
+__device__ __forceinline__ bool in_queries(const AttentionArgs& a, int64_t at, int count) {
+    return QIFT_CK_RANGE(at, count, (a.tokens - 1) * a.q_stride + (int64_t)a.q_heads * a.head_dim);
+}
+__device__ __forceinline__ bool in_result(const AttentionArgs& a, int64_t row) {
+    return QIFT_CK_RANGE(row, 1, a.tokens * a.q_heads);
+}
+__device__ __forceinline__ bool in_parts(const AttentionArgs& a, int slots, int64_t at) {
+    return QIFT_CK_RANGE(at, 1, a.tokens * a.q_heads * slots) &&
+           QIFT_CK_RANGE((at + 1) * a.head_dim * 4, 0, a.workspace_bytes) &&
+           QIFT_CK_RANGE((a.tokens * a.q_heads * slots * a.head_dim + 2 * at) * 4, 8, a.workspace_bytes);
+}
+// ... and a table's entry in the table.
+__device__ __forceinline__ bool in_table(const AttentionArgs& a, bool prefix, int64_t entry) {
+    return QIFT_CK_RANGE(entry, 1, prefix ? ((int64_t)a.prefix_len + (1 << a.log_page) - 1) >> a.log_page : (int64_t)a.max_pages);
+}
+
 // Rotates a row held by a warp, D / 32 contiguous values a lane, by blocks of `block` (0: not).
 template <int D>
 __device__ __forceinline__ void row_hadamard(float (&v)[D / 32], int lane, int block, float norm) {
@@ -240,6 +258,7 @@ __device__ __forceinline__ void finish_row(const AttentionArgs& a, float (&v)[D 
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= inv;
     row_hadamard<D>(v, lane, a.block, a.norm);
+    if (!in_result(a, token * a.q_heads + head)) return;
     const int64_t at = (token * a.q_heads + head) * D + lane * E;
     if (a.f16) {
         __half2 h[E / 2];

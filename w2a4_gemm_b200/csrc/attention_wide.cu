@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 32 / PER; ++q) {
                 const int64_t at = __shfl_sync(0xffffffffu, from, q * PER + lane / PIECES);
                 x[q] = make_uint4(0u, 0u, 0u, 0u);
-                if (at >= 0) x[q] = __ldg(reinterpret_cast<const uint4*>(a.q + at + c * 8));
+                if (at >= 0 && in_queries(a, at + c * 8, 8)) x[q] = __ldg(reinterpret_cast<const uint4*>(a.q + at + c * 8));
             }
 #pragma unroll
             for (int q = 0; q < 32 / PER; ++q) {
@@ -508,12 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float by = (finish ? (sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum)) : 1.0f) *
                              (block ? a.norm : 1.0f);
             const uint64_t by2 = pack2(by, by), minus = pack2(-1.0f, -1.0f);
-            int64_t at = token >= 0 ? token * a.q_heads + head : -1;
+            int64_t at = token >= 0 && in_result(a, token * a.q_heads + head) ? token * a.q_heads + head : -1;
             if (finish) {
-                if (a.lse && token >= 0) a.lse[at] = sum == 0.0f ? -INFINITY : 0.69314718056f * (ref + log2f(sum));
-            } else if (token >= 0) {
+                if (a.lse && at >= 0) a.lse[at] = sum == 0.0f ? -INFINITY : 0.69314718056f * (ref + log2f(sum));
+            } else if (at >= 0) {
                 at = at * deal.slots + (prefix ? split : deal.prefix_splits + split);
-                parts(a, deal.slots).ml[at] = make_float2(ref, sum);
+                if (in_parts(a, deal.slots, at)) parts(a, deal.slots).ml[at] = make_float2(ref, sum);
+                else at = -1;
             }
             float* rows = reinterpret_cast<float*>(smem) + (tile * BM + (warp & 3) * 32) * S::OPAD;
             float* mine = rows + lane * S::OPAD;
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int halves = 2 * __shfl_sync(0xffffffffu, n, 0);
             const uint32_t q0 = desc_low(b32 + t * S::Q_BYTES), k0 = desc_low(b32 + S::K_AT), v0 = desc_low(b32 + S::V_AT);
             const uint32_t t_s = tm + t * BN, t_o = tm + 2 * BN + t * D;
-            const bool one = elect();
+            const bool one = elect() && QIFT_CK((tm & 0xffffu) + 2 * BN + TILES * D <= kTmemCols);
             auto wait_all = [&](uint64_t* on, uint32_t parity) {
                 return __all_sync(0xffffffffu, wait(on, parity, &bar.abort, limit));
             };
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t at = kNowhere;
                 if (i < n && lane < 8) {
                     const int j = block_of(i) * BN + lane * 16;
-                    if (j < range.limit) {
+                    if (j < range.limit && in_table(a, prefix, j >> a.log_page)) {
                         const int page = table[j >> a.log_page];
                         if ((uint32_t)page < (uint64_t)a.n_pages)
                             at = (uint32_t)(((((int64_t)page * a.kv_heads + h) << a.log_page) + (j & ((1 << a.log_page) - 1))) >> 4);

@@ -160,6 +160,7 @@ struct AttentionArgs {
     bool f16;
     float* lse;                 // [tokens][q_heads] or null
     float* workspace;
+    int64_t workspace_bytes;    // read by the bounds-checked build only
 };
 namespace attn {
 // How the blocks of a launch are dealt out: first the prefix's (row tile, kv head, split), then each

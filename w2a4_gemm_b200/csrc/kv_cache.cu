@@ -95,7 +95,8 @@ __device__ __forceinline__ void rope8(float* v, const __half* row, int e, const 
         const bool low = e < half;
         const int at = low ? e : e - half;
         float p[8];
-        load8(*reinterpret_cast<const uint4*>(row + (low ? e + half : e - half)), p);
+        load8(QIFT_CK_RANGE(low ? e + half : e - half, 8, dim)
+                  ? *reinterpret_cast<const uint4*>(row + (low ? e + half : e - half)) : make_uint4(0u, 0u, 0u, 0u), p);
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
             const float4 c4 = *reinterpret_cast<const float4*>(tab + at + j);
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs 
     const int heads = a.q_heads + 2 * a.kv_heads;
     const int64_t position = a.rope && token < a.tokens ? a.positions[token] : 0;
     // A token whose position has no row in the table, or whose slot is not in the cache, is left out.
-    const bool on = token < a.tokens && (!a.rope || (uint64_t)position < (uint64_t)a.rope_len);
+    const bool on = token < a.tokens && (!a.rope || ((uint64_t)position < (uint64_t)a.rope_len &&
+                                                     QIFT_CK_RANGE(position * a.rope_dim, a.rope_dim, a.rope_len * a.rope_dim)));
     const int64_t slot = on ? a.slots[token] : -1;
     const bool kept = (uint64_t)slot < (uint64_t)(a.n_pages << a.log_page);
     const int64_t in_page = ((slot >> a.log_page) * a.kv_heads << a.log_page) + (slot & ((1 << a.log_page) - 1));
@@ -139,6 +141,11 @@ __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs 
     // The row of a head, and whether there is anything to do for it.
     auto row_of = [&](int head) -> const __half* {
         if (!on || head >= heads || (head >= a.q_heads && !kept)) return nullptr;
+        const int of = head < a.q_heads ? 0 : head < a.q_heads + a.kv_heads ? a.q_heads : a.q_heads + a.kv_heads;
+        const int64_t stride = head < a.q_heads ? a.q_stride : head < a.q_heads + a.kv_heads ? a.k_stride : a.v_stride;
+        if (!QIFT_CK_RANGE(token * stride + (int64_t)(head - of) * D, D,
+                           (a.tokens - 1) * stride + (int64_t)(head < a.q_heads ? a.q_heads : a.kv_heads) * D))
+            return nullptr;
         return head < a.q_heads                ? a.q + token * a.q_stride + (int64_t)head * D
                : head < a.q_heads + a.kv_heads ? a.k + token * a.k_stride + (int64_t)(head - a.q_heads) * D
                                                : a.v + token * a.v_stride + (int64_t)(head - a.q_heads - a.kv_heads) * D;
@@ -184,6 +191,7 @@ __global__ void __launch_bounds__(kKvThreads) append_kv_kernel(const AppendArgs 
         for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (!row) continue;
         if (this_head < a.q_heads) {
+            if (!QIFT_CK_RANGE((token * a.q_heads + this_head) * D, D, a.tokens * a.q_heads * D)) continue;
             __half* dst = a.q_out + (token * a.q_heads + this_head) * D + 8 * ts;
             *reinterpret_cast<uint4*>(dst) = packed[0];
             *reinterpret_cast<uint4*>(dst + D / 2) = packed[1];
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kKvThreads) gather_kv_kernel(const GatherArgs 
             v[j] = __fmul_rn(__fsub_rn(__uint_as_float(n), 12582920.0f), s[kv]);
         }
         row_hadamard16<D>(v, ts, a.block, a.norm);
-        if (!there) continue;
+        if (!there || !QIFT_CK_RANGE(row, 1, a.rows)) continue;
         uint4 packed[2];
         __half2* h2 = reinterpret_cast<__half2*>(packed);
 #pragma unroll
