@@ -213,8 +213,10 @@ qift_status qift_decode_linear(const void* x, int64_t tokens, int64_t n_in, int3
  *   codes  : u8 [n_pages][kv_heads][page_size][head_dim/2], for keys and for values; a row holds one
  *            token of one kv head, packed as by qift_quantize_kv (the lower index in the low nibble).
  *   scales : fp32 [n_pages][kv_heads][page_size], s = m / 7 of each row.
- *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096].  Other head dimensions and page
- *   sizes return QIFT_ERR_UNSUPPORTED.  Slot s is token s % page_size of page s / page_size.
+ *   head_dim 64, 128 or 256; page_size a power of two in [16, 4096]; n_pages * kv_heads * page_size at
+ *   most 2^36 - 256.  Other sizes return QIFT_ERR_UNSUPPORTED, and so do calls of more tokens than
+ *   tokens * (q_heads + 2 * kv_heads) < 2^31 (qift_gather_kv: tokens * 2 * kv_heads).  Slot s is token
+ *   s % page_size of page s / page_size.
  *
  * qift_append_kv -- one layer's new tokens: position rotation of queries and keys, Hadamard rotation
  * of queries, keys and values, and symmetric per-row INT4 of keys and values into their slots.
@@ -285,10 +287,11 @@ qift_status qift_gather_kv(const uint8_t* k_cache, const float* k_scales, const 
  *   workspace : device memory of at least qift_paged_attention_workspace() bytes (16-byte aligned),
  *               NULL where that is 0.  Two calls that may run at once, or captured graphs that may,
  *               need one each.
- * Scores, the softmax's sums and the weighted sum are fp32; the weights, times their value's scale,
- * are rounded once to binary16 (2^-11 of each at most) for the tensor cores.  Scales in the cache lie in
- * [0, 65504/7], as qift_append_kv writes them for finite rows; a key with another has an unspecified effect on
- * the rows that see it and none on those that do not.
+ * Scores, the softmax's sums and the weighted sum are fp32.  The weights, times their value's scale, are
+ * rounded once to binary16 for the tensor cores, also where out is fp32: each is off by at most 2^-11 of
+ * itself or 2^-29 of the row's largest, whichever is more (in the latter a value scale below 2^-28 counts
+ * as 2^-28).  Scales in the cache lie in [0, 65504/7], as qift_append_kv writes them for finite rows; a key with
+ * another has an unspecified effect on the rows that see it and none on those that do not.
  * qift_paged_attention_workspace returns the bytes for a call of these sizes, or -1 if qift_paged_attention
  * would refuse them.  head_dim, page_size: as above.  max_pages * page_size + prefix_len <= 2^30;
  * tokens * q_heads and batch * max_q * q_heads < 2^31.

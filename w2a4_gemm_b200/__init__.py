@@ -465,7 +465,8 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
     are.  ``k_cache``/``v_cache`` uint8 ``[pages, kv_heads, page_size, head_dim / 2]`` and ``k_scales``/``v_scales``
     fp32 ``[pages, kv_heads, page_size]`` are written at ``slots`` (int64, ``page * page_size + offset``; -1 =
     padding).  ``rope`` fp32 ``[positions, rope_dim]`` holds cosines, then sines, and ``positions`` (int64) its row
-    for each token.  Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
+    for each token; a token whose position is outside it is left out, its row of a new result not initialised.
+    Returns the rotated queries ``[tokens, q_heads, head_dim]`` (None without ``q``)."""
     if not 0 <= block < 2 ** 31:
         _int32(block=block)
     kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)
@@ -483,7 +484,7 @@ def qift_append_kv(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, block:
             _2d(_cuda(rope, "rope", _F32), "rope")
         rope_len, rope_dim = shape = rope.shape
         rope_at = _is(rope, "rope", _F32, shape, index)
-        if not (rope_len and rope_dim):  # without an address it would pass for no rotation at all
+        if T and not (rope_len and rope_dim):  # without an address it would pass for no rotation at all
             raise ValueError(f"rope must hold at least one position and one pair, got shape {tuple(shape)}")
         positions_at = _is(positions, "positions", _I64, (T,), index)
     if q is not None:
@@ -547,8 +548,9 @@ def qift_paged_attention(q: torch.Tensor, cu_q: torch.Tensor | None, max_q: int,
     ``prefix_table`` (int32): pages of the ``prefix_len`` first keys that all sequences share.  ``block``: the
     result is rotated back by Hadamard blocks of this size (0: left rotated, as ``qift_quantize_acts`` with block
     0 takes it).  ``lse`` (fp32 ``[tokens, q_heads]``), if given, receives the log-sum-exp.  ``workspace`` (uint8,
-    ``qift_paged_attention_workspace`` bytes) is allocated on the call's stream if not given.  Rows of a new result
-    that belong to no sequence are not initialised."""
+    ``qift_paged_attention_workspace`` bytes) is allocated on the call's stream if not given.  The softmax's
+    weights are rounded to binary16 whatever ``out_dtype`` is.  Rows of a new result that belong to no sequence are
+    not initialised."""
     if not 0 <= (max_q | window | sinks | prefix_len | max_kv | block) < 2 ** 31:
         _int32(max_q=max_q, window=window, sinks=sinks, prefix_len=prefix_len, max_kv=max_kv, block=block)
     kc, ks, vc, vs, pages, kv_heads, size, d, index = _cache(k_cache, k_scales, v_cache, v_scales)

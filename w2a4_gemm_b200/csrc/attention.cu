@@ -19,16 +19,18 @@
 // second product: transposing loads pair its codes over two tokens, and they are made exact.
 // Weights: t_j is multiplied into p_j before the rounding to binary16; the running reference is that
 // of u_j + log2 t_j, so the rounded weights lie in [0, 2^15] whatever the size of the values, and
-// keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.
+// keep 11 bits down to 2^-22 of the largest.  The sum of p_j, and O, stay in 32 bits.  Against 64 bits the result is
+// off by 2.9e-4 of its norm, 2.1e-4 of it the rounding of a binary16 result.
 //
 // What bounds it: the bytes of the codes and scales at best (64 sequences of 8000-16384 keys, 32 query and 8
-// key/value heads of 128: 165 us, 5.1 TB/s, 78% of a copy's rate); in fact the chain of a step, codes to scores
-// to weights to products, of which four warps a scheduler run side by side: 465 instructions for 32 keys, 224 of
-// them on the integer pipe at half rate and 160 to make binary16 of nibbles; issue is active 62%, the integer pipe
-// 54%, the tensor pipe 28%.  So a long run of it follows the clock (178-189 us under the power limit).  Tried and slower: shifts as
-// high products on the multiply pipe (186 us for 177 then), five blocks an SM with fewer registers (208),
-// three stages of copies, eight warps a block.  One query head a kv head fills one of eight columns of
-// the products at the same cost a key: 16 sequences of 300-4096 keys by 32 heads take 45 us, 3.4 TB/s.
+// key/value heads of 128: 190 us in a long run, 4.5 TB/s, 68% of a copy's rate); in fact the chain of a step, codes
+// to scores to weights to products, of which four warps a scheduler run side by side: 470 instructions for 32 keys,
+// 224 of them on the integer pipe at half rate and 160 to make binary16 of nibbles; issue is active 62%, the integer
+// pipe 55%, the tensor pipe 28%.  So a run of it follows the clock: a short one, before the power limit, takes
+// 166 us.  Tried and slower: shifts as high products on the multiply pipe (186 us for 177 then, in short runs), five
+// blocks an SM with fewer registers (208), three stages of copies, eight warps a block.  One query head a kv head
+// fills one of eight columns of the products at the same cost a key: 16 sequences of 300-4096 keys by 32 heads take
+// 46 us, 3.3 TB/s.  head_dim 256: the same 64 sequences by 8 kv heads 294 us, 86%, by 2 of 8 query heads 99 us, 63%.
 #include <math.h>
 
 #include <algorithm>
@@ -679,7 +681,11 @@ static Cut cut(bool wide, int per, int64_t kv_heads, int64_t batch, int64_t rows
     c.splits = (int)((steps + c.chunk - 1) / c.chunk);
     // Measured with head_dim 128: a streamed key takes 0.038 ns for a block of 16 rows and 0.024 for one of 8
     // when the GPU is full, a block as much more as 300 keys, a launch 9 us; a step of 256 rows by 128 keys
-    // takes an SM 2.3 us, a launch 17.
+    // takes an SM 2.3 us, a launch 17.  The same constants choose at head_dim 64 (64 and 32 query heads by 8 kv heads,
+    // 16 by 4, 32 by 32; 1, 4 or 16 sequences of 4 to 256 tokens and 300 to 16000 keys, prefixes of 500 to 32000 keys by
+    // up to 256 rows, each size on both kernels): the chosen one took at most 1.37 times the better's time (64
+    // tokens each of 16 sequences of 300 keys, 22.3 us streamed for 16.4), 1% to 2% more on average; at 128 at most
+    // 1.10 times with 8 kv heads, 1.23 with 32.
     const int64_t all = blocks * c.splits;
     c.us = wide ? 17.0 + (double)((all + 147) / 148) * c.chunk * 2.3
                 : 9.0 + (double)all * ((double)c.chunk * kStep + 300.0) * (per == 8 ? 24e-6 : 38e-6) * head_dim / 128;

@@ -25,13 +25,14 @@
 // binary16: the test is the sum of 2^u of each 32 keys, which is needed anyway, times their largest t_j, or times
 // kMostWeight / kMostSum where that is more, so that the sum itself stays below kMostSum.
 //
-// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 581 us, 59% of the
-// measured bf16 matrix rate over the visible half, 614 us in a long run under the power limit): a step of 256
-// rows by 128 keys takes 4000 to 4400 cycles.  S in halves of 64 keys costs the tensor core about 90 cycles a
-// product, half of its rate, since Q is read from shared memory for each; P V 64; together some 3300.  The
-// exponentials of 256 x 128 weights take the special-function unit 2048.  Exponentials on the fp32 pipe (a
-// polynomial for a quarter to a half of the weights) made it slower (690-740 us): the softmax waits for
-// latency, not for that unit.
+// What bounds it, at the prompt of 8192 tokens (32 query and 8 key/value heads of 128; 614 us in a long run under
+// the power limit, 55% of the measured bf16 matrix rate over the visible half; 581 us in a short one): a step of 256
+// rows by 128 keys takes 4000 to 4400 cycles, and a block's start and end come to it.  At its full rate the tensor
+// core would take 2050 of them, and its counter shows that much work (43% of the time); S against 64 keys at a time
+// runs below that rate, since Q is read from shared memory for each half.  The exponentials of 256 x 128 weights
+// take the special-function unit 2048.  Exponentials on the fp32 pipe (a polynomial for a quarter to a half of the
+// weights) made it slower (690-740 us): the softmax waits for latency, not for that unit.  head_dim 64 does half the
+// products a step for as many exponentials: a prompt of 8192 by 64 query heads of 64 takes 1139 us, 30%.
 //
 // Every wait is bounded: one that runs out sets a shared abort flag and the device error word, every
 // role leaves its loop, the products in flight are waited for and tensor memory is freed.
