@@ -926,3 +926,54 @@ def test_append_and_gather_write_nowhere_else(d, rope_dim, interleaved):
     k, v = qg.qift_gather_kv(*cache, slots, d)
     outside = (slots < 0) | (slots >= pages * size)
     assert (k[outside] == 0).all() and (v[outside] == 0).all()
+
+
+def test_no_tokens_need_no_rope_table():
+    cache = empty_cache(1, 1, 16, 64)
+    x, at = torch.empty(0, 1, 64, device="cuda").half(), torch.empty(0, dtype=torch.int64, device="cuda")
+    assert qg.qift_append_kv(x, x, at, 64, *cache, q=x, positions=at, rope=torch.empty(0, 64, device="cuda")).shape == x.shape
+
+
+@pytest.mark.parametrize("path", ["stream", "wide"])
+@pytest.mark.parametrize("d,hk,hq", [(128, 8, 32), (64, 2, 16)])
+def test_steps_that_follow_at_once_see_one_anothers_rows(path, d, hk, hq):
+    """Sixty steps of append and attention one behind the other, with one buffer of queries and one workspace: each
+    kernel may start while the one before it runs, and reads what that one writes (a scale's neighbours in a line too)."""
+    B, steps, size = 4, 60, 16
+    g = gen(41)
+    per = steps // size + 3
+    qkv = torch.randn(steps, B, hq + 2 * hk, d, device="cuda", generator=g).half()
+    table = torch.randperm(B * per, device="cuda", generator=g).to(torch.int32).view(B, per)
+    at = torch.arange(steps, device="cuda")[:, None] + torch.tensor([0, 5, 15, 16], device="cuda")
+    slots = (table.long()[torch.arange(B, device="cuda")[None], at // size] * size + at % size).contiguous()
+    lens = (at + 1).to(torch.int32)
+    rope = rope_table(200, d).cuda()
+    q = torch.empty(B, hq, d, device="cuda").half()
+    qg.qift_debug_set_attention_path(path)
+    workspace = torch.empty(qg.qift_paged_attention_workspace(B, hq, hk, d, B, 1, size, per, prefix_len=0), device="cuda",
+                            dtype=torch.uint8)
+    first = [torch.randint(0, 256, (B * per, hk, size, d // 2), device="cuda", generator=g).to(torch.uint8),
+             torch.rand(B * per, hk, size, device="cuda", generator=g)]
+    first += [x.flip(0).contiguous() for x in first]
+
+    def step(t, cache, out):
+        qg.qift_append_kv(qkv[t][:, hq:hq + hk], qkv[t][:, hq + hk:], slots[t], d, *cache, q=qkv[t][:, :hq], positions=at[t],
+                          rope=rope, q_out=q)
+        qg.qift_paged_attention(q, None, 1, *cache, table, lens[t], block=d, out=out[t], workspace=workspace)
+
+    want, got = torch.empty(2, steps, B, hq, d, device="cuda").half()
+    alone, chained = [c.clone() for c in first], [c.clone() for c in first]
+    for t in range(steps):
+        step(t, alone, want)
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for t in range(steps):
+            step(t, chained, got)
+    for _ in range(10):
+        for a, b in zip(chained, first):
+            a.copy_(b)
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(alone, chained))
